@@ -120,6 +120,14 @@ typedef enum mok_dtype { MOK_F32 = 0, MOK_BF16 = 1, MOK_MXFP8 = 2, MOK_MXFP4 = 3
                                    during the launch. A barrier that does not complete within
                                    its bounded wait leaves MOK_ERR_HIP in the schedule
                                    header's status word; rebuild the schedule after that. */
+#define MOK_FLAG_X_QUANT 16u    /* MX forward: the quantised x rows (xq, xs of mok_mx_layout in this
+                                   micro-batch's forward slot) are already in the workspace, as
+                                   mok_rmsnorm_forward writes them; mok_moe_forward then reads
+                                   neither x nor quantises it, and x may be NULL. The bits are those
+                                   of the call without the flag when the rows are those of x.
+                                   MOK_ERR_DTYPE unless gemm is MX; mok_moe_forward_noalloc, whose
+                                   workspace no caller can fill, refuses it with
+                                   MOK_ERR_WORKSPACE. Other calls ignore it. */
 
 /*
  * Problem descriptor.  Limits: T >= 0; 1 <= k <= min(E, 16); 1 <= E <= 1024;
@@ -356,8 +364,9 @@ mok_status mok_moe_backward(const mok_desc* d, void* sched, const void* x, const
  * (no state shared between threads).  While bound, every launch made by this
  * thread's calls of the kernel group `filter` -- one of "route", "schedule",
  * "fc1", "fc2", "combine", "dh", "router_bwd", "dx", "dx_reduce", "gather",
- * "dw2", "dw1", "dwr", and for MXFP8 "quant" (row quantisers and stash
- * copies), "flush" (block table and token-axis quantisers), or "*" for all --
+ * "dw2", "dw1", "dwr", for MXFP8 "quant" (row quantisers and stash
+ * copies), "flush" (block table and token-axis quantisers), and the operators around the
+ * layer, "norm", or "*" for all --
  * is bracketed by hipEventRecord(events[2n]) before and
  * hipEventRecord(events[2n+1]) after it on the launch stream, for
  * n = count, count + 1, ... < capacity (later launches are not bracketed);
@@ -387,6 +396,59 @@ mok_status mok_trace_bind(mok_trace* t);
  */
 mok_status mok_weights_quantize(const mok_desc* d, const void* w1, const void* w2, const mok_mx_weights* out,
                                 void* stream);
+
+/* ---------------------------------------------------------------------------------------
+ * Operators around the layer step. They follow the conventions at the top of this file
+ * (row-major, contiguous, 16-byte aligned, caller-owned buffers; nothing allocated or
+ * synchronised; arguments checked before anything is enqueued; fixed summation orders, so
+ * repeated calls give the same bits) and need no schedule.
+ * ------------------------------------------------------------------------------------ */
+
+/*
+ * RMS norm with the residual's addition (the norm in front of the layer).
+ *   T rows (0 <= T < 2^31) of H elements: H a multiple of 8, 8 <= H <= 32768 (MOK_ERR_SHAPE).
+ *   act: MOK_F32 or MOK_BF16, the type of every row array and of w.
+ *   quant: equal to act (no quantised output), or MOK_MXFP8 (H a multiple of 128) or MOK_MXFP4
+ *   (of 256) with act = MOK_BF16.  eps >= 0 and finite.  flags: MOK_FLAG_WGRAD_F32 (dw fp32).
+ */
+typedef struct mok_norm_desc {
+  int64_t T;
+  int32_t H;
+  int32_t act;   /* mok_dtype */
+  int32_t quant; /* mok_dtype */
+  uint32_t flags;
+  float eps;
+  int32_t reserved; /* must be 0 */
+} mok_norm_desc;
+
+/* Bytes of the backward workspace.  Pure host computation. */
+mok_status mok_norm_workspace_query(const mok_norm_desc* d, size_t* bwd_ws);
+
+/*
+ * mok_rmsnorm_forward
+ *   v = x + res (res may be NULL: v = x), in fp32;  rstd = 1 / sqrt(mean_h v^2 + eps);
+ *   y = v * rstd * w;  each output is rounded once from fp32:
+ *   r [T][H] (v: the residual stream for the next addition and the backward; may be NULL),
+ *   y [T][H] (may be NULL when quant is MX), rstd [T] fp32 (may be NULL),
+ *   q, s (quant MX, else NULL): y as stored in bf16, quantised in blocks of 32 along H as
+ *   the layer quantises x: q [T][H] E4M3 bytes or [T][H/2] E2M1 pairs, s [H/128][T][4].
+ * r and y may each be the same array as x or as res (not the same as each other); other
+ * overlaps are not allowed.
+ */
+mok_status mok_rmsnorm_forward(const mok_norm_desc* d, const void* x, const void* res, const void* w, void* r, void* y,
+                               void* q, void* s, float* rstd, void* stream);
+
+/*
+ * mok_rmsnorm_backward -- gradients of L = <dy, y> + <dr, r>.  With xh = r * rstd and
+ *   g = dy * w:  dx = dr + rstd * (g - xh * mean_h(g * xh))  (the gradient of x and of res),
+ *   dw_h = sum_t dy * xh.
+ * r [T][H] and rstd [T] as the forward wrote them (r = x without a residual); dr may be NULL
+ * (0).  dx [T][H] may be the same array as dy or dr.  dw [H] in act (fp32 with
+ * MOK_FLAG_WGRAD_F32) may be NULL; every element is written (zero for T = 0).  ws is used
+ * (and required) only with dw.
+ */
+mok_status mok_rmsnorm_backward(const mok_norm_desc* d, const void* dy, const void* dr, const void* r, const void* w,
+                                const float* rstd, void* dx, void* dw, void* ws, size_t ws_bytes, void* stream);
 
 /* Static string naming a status code. */
 const char* mok_status_string(mok_status s);

@@ -2,18 +2,43 @@
 #include <cstring>
 #include <mutex>
 
+#include "api.h"
 #include "kernels.h"
 
 using namespace mok;
 
+namespace mok {
+
+thread_local mok_trace* t_trace = nullptr;
+
+bool trace_on(const char* name) {
+  const mok_trace* t = t_trace;
+  return t != nullptr && t->count >= 0 && t->count < t->capacity &&
+         (std::strcmp(t->filter, "*") == 0 || std::strcmp(t->filter, name) == 0);
+}
+
+// Compute units of the current device, cached per device id.
+mok_status device_cus(int* out) {
+  static std::mutex mu;
+  static int cache[64] = {0};
+  int dev = 0;
+  if (hipGetDevice(&dev) != hipSuccess || dev < 0) return MOK_ERR_HIP;
+  std::lock_guard<std::mutex> lock(mu);
+  if (dev < 64 && cache[dev] > 0) {
+    *out = cache[dev];
+    return MOK_OK;
+  }
+  int cus = 0;
+  if (hipDeviceGetAttribute(&cus, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess || cus <= 0)
+    return MOK_ERR_HIP;
+  if (dev < 64) cache[dev] = cus;
+  *out = cus;
+  return MOK_OK;
+}
+
+}  // namespace mok
+
 namespace {
-
-constexpr size_t kAlign = 256;
-size_t up(size_t v) { return (v + kAlign - 1) & ~(kAlign - 1); }
-
-bool aligned16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
-
-int elem_size(int act) { return act == MOK_F32 ? 4 : 2; }
 
 int mb_count_of(const mok_desc* d) { return d->mb_count > 0 ? d->mb_count : 1; }
 int ring_of(const mok_desc* d) { return d->ring > 0 ? d->ring : 1; }
@@ -43,6 +68,7 @@ mok_status check_desc(const mok_desc* d) {
   if (d->act != MOK_F32 && d->act != MOK_BF16) return MOK_ERR_DTYPE;
   if (d->gemm != d->act && !(is_mx(d) && d->act == MOK_BF16)) return MOK_ERR_DTYPE;
   if ((d->flags & MOK_FLAG_WGRAD_DEFER) && !is_mx(d)) return MOK_ERR_DTYPE;
+  if ((d->flags & MOK_FLAG_X_QUANT) && !is_mx(d)) return MOK_ERR_DTYPE;
   if (d->reserved != 0 || d->mb_count < 0 || d->ring < 0 || d->mb_count > 1024 || d->ring > 1024)
     return MOK_ERR_SHAPE;
   if (d->mb_index < 0 || d->mb_index >= mb_count_of(d)) return MOK_ERR_SHAPE;
@@ -60,25 +86,6 @@ mok_status check_desc(const mok_desc* d) {
   if (d->grid < 0) return MOK_ERR_SHAPE;
   // 32-bit offsets inside the token-axis operands of the MXFP8 weight gradients
   if (is_mx(d) && mx_kmax(d) * std::max<int64_t>(d->H, 2LL * d->I) >= ((int64_t)1 << 31)) return MOK_ERR_SHAPE;
-  return MOK_OK;
-}
-
-// Compute units of the current device, cached per device id.
-mok_status device_cus(int* out) {
-  static std::mutex mu;
-  static int cache[64] = {0};
-  int dev = 0;
-  if (hipGetDevice(&dev) != hipSuccess || dev < 0) return MOK_ERR_HIP;
-  std::lock_guard<std::mutex> lock(mu);
-  if (dev < 64 && cache[dev] > 0) {
-    *out = cache[dev];
-    return MOK_OK;
-  }
-  int cus = 0;
-  if (hipDeviceGetAttribute(&cus, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess || cus <= 0)
-    return MOK_ERR_HIP;
-  if (dev < 64) cache[dev] = cus;
-  *out = cus;
   return MOK_OK;
 }
 
@@ -279,12 +286,6 @@ mok_status make_ctx(const mok_desc* d, const void* sched, void* stream, Ctx* c) 
   return MOK_OK;
 }
 
-#define MOK_REQUIRE(p)                   \
-  do {                                   \
-    if ((p) == nullptr) return MOK_ERR_NULL;  \
-    if (!aligned16(p)) return MOK_ERR_ALIGN; \
-  } while (0)
-
 // ---- workspace of mok_moe_forward_noalloc: a file-scope device array ----
 // In host code `scratch` only names the symbol; its device address (one per GPU, each GPU
 // holds its own copy until the process ends) comes from hipGetSymbolAddress, taken once
@@ -306,33 +307,6 @@ mok_status scratch_ptr(void** out) {
   *out = cache[dev];
   return MOK_OK;
 }
-
-// Buffer sizes passed by the caller against what the descriptor needs.
-mok_status need(size_t have, size_t want) { return have >= want ? MOK_OK : MOK_ERR_WORKSPACE; }
-
-// ---- measurement trace (see mok_trace_bind): the calling thread's caller-owned trace ----
-thread_local mok_trace* t_trace = nullptr;
-
-bool trace_on(const char* name) {
-  const mok_trace* t = t_trace;
-  return t != nullptr && t->count >= 0 && t->count < t->capacity &&
-         (std::strcmp(t->filter, "*") == 0 || std::strcmp(t->filter, name) == 0);
-}
-
-// Launch `call` (a hipError_t expression) bracketed by trace events when traced.
-#define MOK_LAUNCH(name, stream, call)                                                          \
-  do {                                                                                          \
-    const bool tr_ = trace_on(name);                                                            \
-    if (tr_ && hipEventRecord((hipEvent_t)t_trace->events[2 * t_trace->count], stream) != hipSuccess) \
-      return MOK_ERR_HIP;                                                                       \
-    if ((call) != hipSuccess) return MOK_ERR_HIP;                                               \
-    if (tr_) {                                                                                  \
-      if (hipEventRecord((hipEvent_t)t_trace->events[2 * t_trace->count + 1], stream) != hipSuccess) \
-        return MOK_ERR_HIP;                                                                     \
-      t_trace->names[t_trace->count] = name;                                                    \
-      ++t_trace->count;                                                                         \
-    }                                                                                           \
-  } while (0)
 
 // MX backward of micro-batch d->mb_index (see mok_moe_backward in mok.h).
 mok_status mx_backward(const mok_desc* d, const Ctx& c, const void* x, const int32_t* idx, const float* gate,
@@ -539,7 +513,8 @@ mok_status mok_moe_forward(const mok_desc* d, void* sched, const void* x, const 
   st = make_ctx(d, sched, stream, &c);
   if (st != MOK_OK) return st;
   if (c.R == 0) return MOK_OK;
-  MOK_REQUIRE(x);
+  const bool xquant = (d->flags & MOK_FLAG_X_QUANT) != 0;  // the x rows are in the workspace, quantised
+  if (!xquant) MOK_REQUIRE(x);
   MOK_REQUIRE(gate);
   MOK_REQUIRE(y);
   if (!is_replay(d)) MOK_REQUIRE(saved);
@@ -560,7 +535,7 @@ mok_status mok_moe_forward(const mok_desc* d, void* sched, const void* x, const 
       au = fs + X.rau;
       hr = fs + X.rh;
     }
-    MOK_LAUNCH("quant", c.s, launch_mx_quant_rows(c, x, c.T, c.H, fs + X.xq, fs + X.xs, c.T));
+    if (!xquant) MOK_LAUNCH("quant", c.s, launch_mx_quant_rows(c, x, c.T, c.H, fs + X.xq, fs + X.xs, c.T));
     MOK_LAUNCH("fc1", c.s, launch_fc1_mx(c, fs + X.xq, fs + X.xs, q->w1q, q->w1s, au, hr, fs + X.hq, fs + X.hs));
     MOK_LAUNCH("fc2", c.s, launch_fc2_mx(c, fs + X.hq, fs + X.hs, q->w2q, q->w2s, fs + X.part));
     MOK_LAUNCH("combine", c.s, launch_combine(c, fs + X.part, gate, y));
@@ -584,7 +559,7 @@ mok_status mok_moe_forward_noalloc(const mok_desc* d, void* sched, const void* x
   mok_sizes sz;
   mok_status st = mok_workspace_query(d, &sz);
   if (st != MOK_OK) return st;
-  if (sz.fwd_ws > kScratchBytes) return MOK_ERR_WORKSPACE;
+  if (sz.fwd_ws > kScratchBytes || (d->flags & MOK_FLAG_X_QUANT)) return MOK_ERR_WORKSPACE;
   void* ws = nullptr;
   if ((st = scratch_ptr(&ws)) != MOK_OK) return st;
   return mok_moe_forward(d, sched, x, gate, w, y, saved, saved_bytes, ws, kScratchBytes, stream);

@@ -22,6 +22,7 @@ FLAG_WGRAD_F32 = 1
 FLAG_WGRAD_DEFER = 2
 FLAG_REPLAY = 4
 FLAG_FUSED = 8
+FLAG_X_QUANT = 16
 DTYPES = {"f32": F32, "bf16": BF16, "mxfp8": MXFP8, "mxfp4": MXFP4}
 TORCH_DTYPE = {F32: torch.float32, BF16: torch.bfloat16}
 
@@ -76,6 +77,11 @@ class _SavedLayout(ctypes.Structure):
     _fields_ = [("au_offset", ctypes.c_size_t), ("h_offset", ctypes.c_size_t)]
 
 
+class _NormDesc(ctypes.Structure):
+    _fields_ = [("T", ctypes.c_int64), ("H", ctypes.c_int32), ("act", ctypes.c_int32), ("quant", ctypes.c_int32),
+                ("flags", ctypes.c_uint32), ("eps", ctypes.c_float), ("reserved", ctypes.c_int32)]
+
+
 MX_LAYOUT_FIELDS = ("fwd_slot", "xq", "xs", "hq", "hs", "bwd_slot", "dyq", "dys", "dguq", "dgus", "st_xs", "st_dos",
                     "st_h", "st_dgu", "pofs", "dot", "dots", "ht", "hts", "dgut", "dguts", "xt", "xts")
 
@@ -104,6 +110,9 @@ def _load():
         "mok_moe_backward": [D, P, P, P, P, ctypes.POINTER(_Weights), P, P, Z, P, P, P, P, P, P, P, Z, P],
         "mok_trace_bind": [ctypes.POINTER(_Trace)],
         "mok_weights_quantize": [D, P, P, ctypes.POINTER(_MxWeights), P],
+        "mok_norm_workspace_query": [ctypes.POINTER(_NormDesc), ctypes.POINTER(Z)],
+        "mok_rmsnorm_forward": [ctypes.POINTER(_NormDesc)] + [P] * 9,
+        "mok_rmsnorm_backward": [ctypes.POINTER(_NormDesc)] + [P] * 8 + [Z, P],
     }
     for name, args in sig.items():
         f = getattr(lib, name)
@@ -120,7 +129,8 @@ _lib = _load()
 EXPORTS = ("mok_workspace_query", "mok_schedule_layout_query", "mok_saved_layout_query", "mok_mx_layout_query",
            "mok_route",
            "mok_schedule_build", "mok_moe_forward", "mok_moe_forward_noalloc", "mok_moe_backward",
-           "mok_weights_quantize", "mok_status_string", "mok_version", "mok_trace_bind")
+           "mok_weights_quantize", "mok_status_string", "mok_version", "mok_trace_bind",
+           "mok_norm_workspace_query", "mok_rmsnorm_forward", "mok_rmsnorm_backward")
 NOALLOC_WS_BYTES = 32 << 20
 
 
@@ -267,6 +277,16 @@ def weights_quantize(d: Desc, w1, w2, mxw: MxWeights, stream=None):
            "mok_weights_quantize")
 
 
+def x_quant_views(d: Desc, fwd_ws):
+    """The quantised x rows of micro-batch d.mb_index in the forward workspace: q [T, H] (MXFP4: [T, H/2]) and
+    s [H/128, T, 4], where rmsnorm_forward writes them for a moe_forward with FLAG_X_QUANT."""
+    L = mx_layout_query(d)
+    o = (d.mb_index % d.ring) * L["fwd_slot"]
+    hq = d.H // 2 if d.gemm == MXFP4 else d.H
+    q = fwd_ws[o + L["xq"]: o + L["xq"] + d.T * hq].view(d.T, hq)
+    return q, fwd_ws[o + L["xs"]: o + L["xs"] + d.T * d.H // 32].view(d.H // 128, d.T, 4)
+
+
 def _weights(w1, w2, mxw):
     q = None if mxw is None else mxw.c()
     w = _Weights(None if w1 is None else w1.data_ptr(), None if w2 is None else w2.data_ptr(),
@@ -293,6 +313,105 @@ def moe_backward(d: Desc, sched, x, idx, gate, w1, w2, wr, saved, dy, dx, dw1, d
     _check(_lib.mok_moe_backward(ctypes.byref(d.c()), _p(sched), _p(x), _p(idx), _p(gate), ctypes.byref(w), _p(wr),
                                  _p(saved), _nb(saved), _p(dy), _p(dx), _p(dw1), _p(dw2), _p(dgate), _p(dwr), _p(ws),
                                  _nb(ws), _stream(stream)), "mok_moe_backward")
+
+
+# ---------------------------------------------------------------------------
+# Operators around the layer step. Their descriptors are immutable and keep the C
+# structure; their calls check every tensor's type, shape, contiguity and device
+# (ValueError) before the library checks the rest (MokError), and run on the
+# tensors' device.
+# ---------------------------------------------------------------------------
+
+def _ptr(name: str, t, dtype, shape, dev, optional=False):
+    """Device pointer of a tensor after the checks of the operators around the layer."""
+    if t is None:
+        if optional:
+            return None
+        raise ValueError("%s is required" % name)
+    if t.dtype is not dtype or t.shape != shape:
+        raise ValueError("%s: expected %s %s, got %s %s" % (name, dtype, tuple(shape), t.dtype, tuple(t.shape)))
+    if not t.is_contiguous():
+        raise ValueError("%s: not contiguous" % name)
+    if t.device != dev:
+        raise ValueError("%s: on %s, expected %s" % (name, t.device, dev))
+    return t.data_ptr()
+
+
+def _ws(t, dev):
+    """(pointer, bytes) of a workspace tensor."""
+    if t is None:
+        return None, 0
+    if not t.is_contiguous() or t.device != dev:
+        raise ValueError("ws: expected a contiguous tensor on %s" % dev)
+    return t.data_ptr(), t.numel() * t.element_size()
+
+
+def _run(fn, where: str, dev, stream, *args):
+    """Call a library function with the arguments and a stream of device `dev`, which is made current."""
+    if dev.type != "cuda":
+        raise ValueError("%s: tensors must be on the GPU, got %s" % (where, dev))
+    if dev.index != torch.cuda.current_device():
+        with torch.cuda.device(dev):
+            return _run(fn, where, dev, stream, *args)
+    s = torch.cuda.current_stream(dev) if stream is None else stream
+    st = fn(*args, s.cuda_stream)
+    if st != 0:
+        _check(st, where)
+
+
+@dataclass(frozen=True)
+class NormDesc:
+    """RMS norm of T rows of H elements (mok_norm_desc); quant: None, MXFP8 or MXFP4."""
+    T: int
+    H: int
+    act: int = BF16
+    quant: Optional[int] = None
+    eps: float = 1e-6
+    flags: int = 0
+
+    def __post_init__(self):
+        q = self.act if self.quant is None else self.quant
+        object.__setattr__(self, "_c", _NormDesc(self.T, self.H, self.act, q, self.flags, self.eps, 0))
+
+    def c(self) -> _NormDesc:
+        return self._c
+
+    @property
+    def dtype(self) -> torch.dtype:
+        return TORCH_DTYPE[self.act]
+
+
+def norm_workspace_query(d: NormDesc) -> dict:
+    n = ctypes.c_size_t()
+    _check(_lib.mok_norm_workspace_query(d._c, n), "mok_norm_workspace_query")
+    return dict(bwd_ws=n.value)
+
+
+def rmsnorm_forward(d: NormDesc, x, w, y=None, res=None, r=None, q=None, s=None, rstd=None, stream=None):
+    """r = x + res; y = r * rstd * w; q, s = the MX rows of y (q [T, H] or, MXFP4, [T, H/2] bytes, s [H/128, T, 4])."""
+    T, H, t, dev, u8 = d.T, d.H, TORCH_DTYPE.get(d.act), x.device, torch.uint8
+    rows = (T, H)
+    mx = d.quant in (MXFP8, MXFP4)
+    if not mx and (q is not None or s is not None):
+        raise ValueError("q, s: the descriptor has no MX output")
+    _run(_lib.mok_rmsnorm_forward, "mok_rmsnorm_forward", dev, stream, d._c, _ptr("x", x, t, rows, dev),
+         _ptr("res", res, t, rows, dev, True), _ptr("w", w, t, (H,), dev), _ptr("r", r, t, rows, dev, True),
+         _ptr("y", y, t, rows, dev, mx),
+         _ptr("q", q, u8, (T, H // 2) if d.quant == MXFP4 else rows, dev) if mx else None,
+         _ptr("s", s, u8, (H // 128, T, 4), dev) if mx else None,
+         _ptr("rstd", rstd, torch.float32, (T,), dev, True))
+
+
+def rmsnorm_backward(d: NormDesc, dy, r, w, rstd, dx, dw=None, dr=None, ws=None, stream=None):
+    """dx = dr + rstd * (g - xh * mean(g * xh)), dw = sum dy * xh, with xh = r * rstd and g = dy * w."""
+    T, H, t, dev = d.T, d.H, TORCH_DTYPE.get(d.act), dy.device
+    rows = (T, H)
+    wt = torch.float32 if d.flags & FLAG_WGRAD_F32 else t
+    wp, wn = _ws(ws, dev)
+    _run(_lib.mok_rmsnorm_backward, "mok_rmsnorm_backward", dev, stream, d._c, _ptr("dy", dy, t, rows, dev),
+         _ptr("dr", dr, t, rows, dev, True), _ptr("r", r, t, rows, dev), _ptr("w", w, t, (H,), dev),
+         _ptr("rstd", rstd, torch.float32, (T,), dev), _ptr("dx", dx, t, rows, dev), _ptr("dw", dw, wt, (H,), dev, True),
+         wp, wn)
 
 
 class KernelTrace:
