@@ -366,7 +366,7 @@ mok_status mok_moe_backward(const mok_desc* d, void* sched, const void* x, const
  * "fc1", "fc2", "combine", "dh", "router_bwd", "dx", "dx_reduce", "gather",
  * "dw2", "dw1", "dwr", for MXFP8 "quant" (row quantisers and stash
  * copies), "flush" (block table and token-axis quantisers), and the operators around the
- * layer, "norm", or "*" for all --
+ * layer, "norm", "balance", or "*" for all --
  * is bracketed by hipEventRecord(events[2n]) before and
  * hipEventRecord(events[2n+1]) after it on the launch stream, for
  * n = count, count + 1, ... < capacity (later launches are not bracketed);
@@ -449,6 +449,64 @@ mok_status mok_rmsnorm_forward(const mok_norm_desc* d, const void* x, const void
  */
 mok_status mok_rmsnorm_backward(const mok_norm_desc* d, const void* dy, const void* dr, const void* r, const void* w,
                                 const float* rstd, void* dx, void* dw, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * Balance loss of the router, per-expert counts, and the gradient by the router's logits.
+ *   T tokens (0 <= T < 2^31), E experts (1..1024), k slots (1..min(E,16)).
+ *   S: number of sequences (segments of consecutive tokens), 0..65535.  seg [S+1] int32 holds
+ *   their offsets: segment s is tokens seg[s] .. seg[s+1]-1, 0 <= seg[0] <= ... <= seg[S] <= T
+ *   (anything else gives unspecified results inside the arrays).  S = 0: one segment of all T
+ *   tokens, seg is not read; arrays over segments then have one row (S below means 1).
+ *   mask [T] bytes or NULL: a token of mask 0 does not count, nor does one in no segment.
+ *   Such tokens' logits and idx are not used, and their dlogits are written as 0.
+ *   score: MOK_SCORE_SOFTMAX  p_te = exp(z_te) / sum_f exp(z_tf)
+ *          MOK_SCORE_SIGMOID  p_te = sig(z_te) / sum_f sig(z_tf)
+ *   (a token whose every logit is -inf has p = 0, no gradient and no z term.)
+ *   grad: type of dlogits, MOK_F32 or MOK_BF16.  coef, zcoef finite; zcoef = 0 unless softmax.
+ *
+ *   n_s counted tokens of segment s, c_se their slots with idx = e (a slot whose idx is
+ *   outside [0, E) counts for no expert), Pm_se = (1/n_s) sum_t p_te,
+ *   S' = segments with n_s > 0, N = sum_s n_s:
+ *   loss[0] = coef / S' * sum_s E * sum_e c_se / (k n_s) * Pm_se      (0 for S' = 0)
+ *   loss[1] = zcoef / N * sum_t (log sum_e exp z_te)^2                (0 for N = 0)
+ */
+typedef enum mok_score { MOK_SCORE_SOFTMAX = 0, MOK_SCORE_SIGMOID = 1 } mok_score;
+
+typedef struct mok_balance_desc {
+  int64_t T;
+  int32_t E, k, S;
+  int32_t score; /* mok_score */
+  int32_t grad;  /* mok_dtype */
+  float coef, zcoef;
+  int32_t reserved; /* must be 0 */
+} mok_balance_desc;
+
+/* Bytes of the forward workspace.  Pure host computation. */
+mok_status mok_balance_workspace_query(const mok_balance_desc* d, size_t* fwd_ws);
+
+/*
+ * mok_balance_forward -- logits [T][E] fp32 (as mok_route writes them), idx [T][k] int32.
+ * Writes loss [2] fp32, counts [S][E] int32 (c), tokens [S+2] int32 (n_0.., then S' and N),
+ * prob [S][E] fp32 (Pm; 0 where n_s = 0) and stat [T] fp32 (per counted token, for the
+ * backward: log sum_f exp(z_tf - max_e z_te), or with MOK_SCORE_SIGMOID
+ * exp(-min(max_e z_te, 0)) sum_f sig(z_tf); other tokens' are left as they were).  Sums over tokens are held in fp32 over at most T/512 rows of a workgroup and
+ * in fp64 beyond.
+ */
+mok_status mok_balance_forward(const mok_balance_desc* d, const float* logits, const int32_t* idx, const int32_t* seg,
+                               const uint8_t* mask, float* loss, int32_t* counts, int32_t* tokens, float* prob,
+                               float* stat, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * mok_balance_backward -- dlogits [T][E] of dloss[0] * loss[0] + dloss[1] * loss[1], dloss [2]
+ * fp32 on the device; counts, tokens and stat as the forward wrote them.  The counts are
+ * constants of the gradient (top-k selection is not differentiated).  With
+ * G_s = dloss[0] * coef * E / (S' k n_s^2):
+ *   softmax  dz_te = p_te * (G_s (c_se - sum_f p_tf c_sf) + dloss[1] * zcoef * 2/N * log sum_f exp z_tf)
+ *   sigmoid  dz_te = p_te * (1 - sig(z_te)) * G_s (c_se - sum_f p_tf c_sf)
+ */
+mok_status mok_balance_backward(const mok_balance_desc* d, const float* logits, const int32_t* seg, const uint8_t* mask,
+                                const int32_t* counts, const int32_t* tokens, const float* stat, const float* dloss,
+                                void* dlogits, void* stream);
 
 /* Static string naming a status code. */
 const char* mok_status_string(mok_status s);

@@ -22,6 +22,34 @@ mok_status check_norm(const mok_norm_desc* d) {
   return MOK_OK;
 }
 
+mok_status check_balance(const mok_balance_desc* d) {
+  if (d == nullptr) return MOK_ERR_NULL;
+  if (d->grad != MOK_F32 && d->grad != MOK_BF16) return MOK_ERR_DTYPE;
+  if (d->score != MOK_SCORE_SOFTMAX && d->score != MOK_SCORE_SIGMOID) return MOK_ERR_DTYPE;
+  if (d->reserved != 0) return MOK_ERR_SHAPE;
+  if (d->T < 0 || d->T >= ((int64_t)1 << 31) || d->E < 1 || d->E > 1024) return MOK_ERR_SHAPE;
+  if (d->k < 1 || d->k > 16 || d->k > d->E || d->S < 0 || d->S > 65535) return MOK_ERR_SHAPE;
+  if (!std::isfinite(d->coef) || !std::isfinite(d->zcoef)) return MOK_ERR_SHAPE;
+  if (d->zcoef != 0.0f && d->score != MOK_SCORE_SOFTMAX) return MOK_ERR_SHAPE;
+  return MOK_OK;
+}
+
+BalanceArgs balance_args(const mok_balance_desc* d, const float* logits, const int32_t* seg, const uint8_t* mask) {
+  BalanceArgs a{};
+  a.T = d->T;
+  a.E = d->E;
+  a.k = d->k;
+  a.S = std::max(d->S, 1);
+  a.sigmoid = d->score == MOK_SCORE_SIGMOID;
+  a.bf16_grad = d->grad == MOK_BF16;
+  a.coef = d->coef;
+  a.zcoef = d->zcoef;
+  a.logits = logits;
+  a.seg = d->S > 0 ? seg : nullptr;
+  a.mask = mask;
+  return a;
+}
+
 }  // namespace
 
 // A pointer that may be NULL, aligned when it is not.
@@ -105,6 +133,77 @@ mok_status mok_rmsnorm_backward(const mok_norm_desc* d, const void* dy, const vo
     MOK_LAUNCH("norm", (hipStream_t)stream,
                launch_col_sum((const float*)ws, norm_parts(d->T, d->H, d->act), d->H, dw,
                               d->act == MOK_F32 || (d->flags & MOK_FLAG_WGRAD_F32) != 0, (hipStream_t)stream));
+  return MOK_OK;
+}
+
+mok_status mok_balance_workspace_query(const mok_balance_desc* d, size_t* fwd_ws) {
+  mok_status st = check_balance(d);
+  if (st != MOK_OK) return st;
+  if (fwd_ws == nullptr) return MOK_ERR_NULL;
+  *fwd_ws = balance_ws(d->T, d->E, std::max(d->S, 1)).bytes;
+  return MOK_OK;
+}
+
+mok_status mok_balance_forward(const mok_balance_desc* d, const float* logits, const int32_t* idx, const int32_t* seg,
+                               const uint8_t* mask, float* loss, int32_t* counts, int32_t* tokens, float* prob,
+                               float* stat, void* ws, size_t ws_bytes, void* stream) {
+  size_t want = 0;
+  mok_status st = mok_balance_workspace_query(d, &want);
+  if (st != MOK_OK) return st;
+  if ((st = need(ws_bytes, want)) != MOK_OK) return st;
+  if (d->T > 0) {
+    MOK_REQUIRE(logits);
+    MOK_REQUIRE(idx);
+    MOK_REQUIRE(stat);
+  }
+  if (d->S > 0) MOK_REQUIRE(seg);
+  MOK_OPTIONAL(mask);
+  MOK_REQUIRE(loss);
+  MOK_REQUIRE(counts);
+  MOK_REQUIRE(tokens);
+  MOK_REQUIRE(prob);
+  MOK_REQUIRE(ws);
+  BalanceArgs a = balance_args(d, logits, seg, mask);
+  const BalanceWs w = balance_ws(a.T, a.E, a.S);
+  char* wb = (char*)ws;
+  a.rows = w.rows;
+  a.chunks = w.chunks;
+  a.idx = idx;
+  a.loss = loss;
+  a.counts = counts;
+  a.tokens = tokens;
+  a.prob = prob;
+  a.stat = stat;
+  a.wq = (float*)(wb + w.q);
+  a.wc = (int32_t*)(wb + w.c);
+  a.wn = (int32_t*)(wb + w.n);
+  a.wz = (float*)(wb + w.z);
+  a.wl = (double*)(wb + w.loss);
+  MOK_LAUNCH("balance", (hipStream_t)stream, launch_balance_fwd(a, (hipStream_t)stream));
+  return MOK_OK;
+}
+
+mok_status mok_balance_backward(const mok_balance_desc* d, const float* logits, const int32_t* seg, const uint8_t* mask,
+                                const int32_t* counts, const int32_t* tokens, const float* stat, const float* dloss,
+                                void* dlogits, void* stream) {
+  mok_status st = check_balance(d);
+  if (st != MOK_OK) return st;
+  if (d->T == 0) return MOK_OK;  // empty arrays may be NULL
+  MOK_REQUIRE(logits);
+  if (d->S > 0) MOK_REQUIRE(seg);
+  MOK_OPTIONAL(mask);
+  MOK_REQUIRE(counts);
+  MOK_REQUIRE(tokens);
+  MOK_REQUIRE(stat);
+  MOK_REQUIRE(dloss);
+  MOK_REQUIRE(dlogits);
+  BalanceArgs a = balance_args(d, logits, seg, mask);
+  a.counts = const_cast<int32_t*>(counts);
+  a.tokens = const_cast<int32_t*>(tokens);
+  a.stat = const_cast<float*>(stat);
+  a.dloss = dloss;
+  a.dlogits = dlogits;
+  MOK_LAUNCH("balance", (hipStream_t)stream, launch_balance_bwd(a, (hipStream_t)stream));
   return MOK_OK;
 }
 

@@ -23,6 +23,8 @@ FLAG_WGRAD_DEFER = 2
 FLAG_REPLAY = 4
 FLAG_FUSED = 8
 FLAG_X_QUANT = 16
+SCORE_SOFTMAX, SCORE_SIGMOID = 0, 1
+SCORES = {"softmax": SCORE_SOFTMAX, "sigmoid": SCORE_SIGMOID}
 DTYPES = {"f32": F32, "bf16": BF16, "mxfp8": MXFP8, "mxfp4": MXFP4}
 TORCH_DTYPE = {F32: torch.float32, BF16: torch.bfloat16}
 
@@ -82,6 +84,12 @@ class _NormDesc(ctypes.Structure):
                 ("flags", ctypes.c_uint32), ("eps", ctypes.c_float), ("reserved", ctypes.c_int32)]
 
 
+class _BalanceDesc(ctypes.Structure):
+    _fields_ = [("T", ctypes.c_int64), ("E", ctypes.c_int32), ("k", ctypes.c_int32), ("S", ctypes.c_int32),
+                ("score", ctypes.c_int32), ("grad", ctypes.c_int32), ("coef", ctypes.c_float),
+                ("zcoef", ctypes.c_float), ("reserved", ctypes.c_int32)]
+
+
 MX_LAYOUT_FIELDS = ("fwd_slot", "xq", "xs", "hq", "hs", "bwd_slot", "dyq", "dys", "dguq", "dgus", "st_xs", "st_dos",
                     "st_h", "st_dgu", "pofs", "dot", "dots", "ht", "hts", "dgut", "dguts", "xt", "xts")
 
@@ -113,6 +121,9 @@ def _load():
         "mok_norm_workspace_query": [ctypes.POINTER(_NormDesc), ctypes.POINTER(Z)],
         "mok_rmsnorm_forward": [ctypes.POINTER(_NormDesc)] + [P] * 9,
         "mok_rmsnorm_backward": [ctypes.POINTER(_NormDesc)] + [P] * 8 + [Z, P],
+        "mok_balance_workspace_query": [ctypes.POINTER(_BalanceDesc), ctypes.POINTER(Z)],
+        "mok_balance_forward": [ctypes.POINTER(_BalanceDesc)] + [P] * 10 + [Z, P],
+        "mok_balance_backward": [ctypes.POINTER(_BalanceDesc)] + [P] * 9,
     }
     for name, args in sig.items():
         f = getattr(lib, name)
@@ -130,7 +141,8 @@ EXPORTS = ("mok_workspace_query", "mok_schedule_layout_query", "mok_saved_layout
            "mok_route",
            "mok_schedule_build", "mok_moe_forward", "mok_moe_forward_noalloc", "mok_moe_backward",
            "mok_weights_quantize", "mok_status_string", "mok_version", "mok_trace_bind",
-           "mok_norm_workspace_query", "mok_rmsnorm_forward", "mok_rmsnorm_backward")
+           "mok_norm_workspace_query", "mok_rmsnorm_forward", "mok_rmsnorm_backward",
+           "mok_balance_workspace_query", "mok_balance_forward", "mok_balance_backward")
 NOALLOC_WS_BYTES = 32 << 20
 
 
@@ -412,6 +424,60 @@ def rmsnorm_backward(d: NormDesc, dy, r, w, rstd, dx, dw=None, dr=None, ws=None,
          _ptr("dr", dr, t, rows, dev, True), _ptr("r", r, t, rows, dev), _ptr("w", w, t, (H,), dev),
          _ptr("rstd", rstd, torch.float32, (T,), dev), _ptr("dx", dx, t, rows, dev), _ptr("dw", dw, wt, (H,), dev, True),
          wp, wn)
+
+
+@dataclass(frozen=True)
+class BalanceDesc:
+    """Balance loss over T tokens and E experts (mok_balance_desc); S sequences, or 0 for one of all tokens."""
+    T: int
+    E: int
+    k: int
+    S: int = 0
+    score: int = SCORE_SOFTMAX
+    grad: int = F32
+    coef: float = 1.0
+    zcoef: float = 0.0
+
+    def __post_init__(self):
+        object.__setattr__(self, "_c", _BalanceDesc(self.T, self.E, self.k, self.S, self.score, self.grad, self.coef,
+                                                    self.zcoef, 0))
+
+    def c(self) -> _BalanceDesc:
+        return self._c
+
+
+def balance_workspace_query(d: BalanceDesc) -> dict:
+    n = ctypes.c_size_t()
+    _check(_lib.mok_balance_workspace_query(d._c, n), "mok_balance_workspace_query")
+    return dict(fwd_ws=n.value)
+
+
+def _mask(t, T, dev):
+    if t is not None and t.dtype is torch.bool:
+        t = t.view(torch.uint8)
+    return _ptr("mask", t, torch.uint8, (T,), dev, True)
+
+
+def balance_forward(d: BalanceDesc, logits, idx, loss, counts, tokens, prob, stat, ws, seg=None, mask=None, stream=None):
+    """loss [2], counts [S, E], tokens [S + 2], prob [S, E] and stat [T] from the router's logits [T, E] and idx [T, k];
+    seg: offsets [S + 1] of the sequences, mask: [T] uint8 or bool."""
+    T, E, S, dev, f32, i32 = d.T, d.E, max(d.S, 1), logits.device, torch.float32, torch.int32
+    wp, wn = _ws(ws, dev)
+    _run(_lib.mok_balance_forward, "mok_balance_forward", dev, stream, d._c, _ptr("logits", logits, f32, (T, E), dev),
+         _ptr("idx", idx, i32, (T, d.k), dev), _ptr("seg", seg, i32, (S + 1,), dev) if d.S > 0 else None,
+         _mask(mask, T, dev), _ptr("loss", loss, f32, (2,), dev), _ptr("counts", counts, i32, (S, E), dev),
+         _ptr("tokens", tokens, i32, (S + 2,), dev), _ptr("prob", prob, f32, (S, E), dev),
+         _ptr("stat", stat, f32, (T,), dev), wp, wn)
+
+
+def balance_backward(d: BalanceDesc, logits, counts, tokens, stat, dloss, dlogits, seg=None, mask=None, stream=None):
+    """dlogits [T, E] (fp32, or bf16 with grad = BF16) of dloss[0] * loss[0] + dloss[1] * loss[1]."""
+    T, E, S, dev, f32, i32 = d.T, d.E, max(d.S, 1), logits.device, torch.float32, torch.int32
+    _run(_lib.mok_balance_backward, "mok_balance_backward", dev, stream, d._c, _ptr("logits", logits, f32, (T, E), dev),
+         _ptr("seg", seg, i32, (S + 1,), dev) if d.S > 0 else None, _mask(mask, T, dev),
+         _ptr("counts", counts, i32, (S, E), dev), _ptr("tokens", tokens, i32, (S + 2,), dev),
+         _ptr("stat", stat, f32, (T,), dev), _ptr("dloss", dloss, f32, (2,), dev),
+         _ptr("dlogits", dlogits, TORCH_DTYPE.get(d.grad), (T, E), dev))
 
 
 class KernelTrace:
