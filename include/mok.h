@@ -366,7 +366,7 @@ mok_status mok_moe_backward(const mok_desc* d, void* sched, const void* x, const
  * "fc1", "fc2", "combine", "dh", "router_bwd", "dx", "dx_reduce", "gather",
  * "dw2", "dw1", "dwr", for MXFP8 "quant" (row quantisers and stash
  * copies), "flush" (block table and token-axis quantisers), and the operators around the
- * layer, "norm", "balance", or "*" for all --
+ * layer, "norm", "balance", "linear", or "*" for all --
  * is bracketed by hipEventRecord(events[2n]) before and
  * hipEventRecord(events[2n+1]) after it on the launch stream, for
  * n = count, count + 1, ... < capacity (later launches are not bracketed);
@@ -507,6 +507,64 @@ mok_status mok_balance_forward(const mok_balance_desc* d, const float* logits, c
 mok_status mok_balance_backward(const mok_balance_desc* d, const float* logits, const int32_t* seg, const uint8_t* mask,
                                 const int32_t* counts, const int32_t* tokens, const float* stat, const float* dloss,
                                 void* dlogits, void* stream);
+
+/*
+ * Matrix product with bias, activation and residual in its epilogue, and its gradients: the
+ * dense (shared) expert beside the routed ones, its second product with the layer's y as the
+ * residual, and the product that takes the gradient of the router's logits into dx and dWr.
+ *   M rows (0 <= M < 2^31), K inputs, N outputs: N, K multiples of 8, 8 .. 2^20, every matrix
+ *   below 2^38 elements (MOK_ERR_SHAPE).
+ *   act: MOK_F32 or MOK_BF16, the type of x, w, res, y, pre, dy, dx and dx_add.
+ *   epi, with P = 2N for MOK_EPI_SWIGLU and P = N else:
+ *     MOK_EPI_NONE   f(p) = p             MOK_EPI_SILU  f(p) = p sig(p)
+ *     MOK_EPI_GELU   f(p) = p Phi(p)      (Phi: the normal distribution function, by erf)
+ *     MOK_EPI_SWIGLU f(p) = silu(p[0..N-1]) * p[N..2N-1]  (gate columns, then up columns, as w1)
+ *   flags: MOK_FLAG_WGRAD_F32 (dw, dw_add fp32 instead of act).
+ */
+typedef enum mok_epilogue {
+  MOK_EPI_NONE = 0,
+  MOK_EPI_SILU = 1,
+  MOK_EPI_GELU = 2,
+  MOK_EPI_SWIGLU = 3
+} mok_epilogue;
+
+typedef struct mok_linear_desc {
+  int64_t M;
+  int32_t N, K;
+  int32_t act;  /* mok_dtype */
+  int32_t epi;  /* mok_epilogue */
+  uint32_t flags;
+  int32_t reserved; /* must be 0 */
+} mok_linear_desc;
+
+typedef struct mok_linear_sizes {
+  size_t fwd_ws; /* partial products of a split K */
+  size_t bwd_ws; /* dpre rows [M][P], bias-gradient parts, partial products */
+} mok_linear_sizes;
+
+/* Bytes of the workspaces.  Pure host computation. */
+mok_status mok_linear_workspace_query(const mok_linear_desc* d, mok_linear_sizes* sizes);
+
+/*
+ * mok_linear_forward -- p = x w^T + bias;  y = f(p) + res, in fp32, rounded once.
+ * x [M][K], w [P][K], bias [P] fp32 or NULL, res [M][N] or NULL (may be the same array as
+ * y), y [M][N], pre [M][P] (p, for the backward) or NULL.
+ */
+mok_status mok_linear_forward(const mok_linear_desc* d, const void* x, const void* w, const float* bias,
+                              const void* res, void* y, void* pre, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * mok_linear_backward -- gradients of L = <dy, y>.  dp = dy f'(pre), rounded to act (the
+ * products' operand; exact for MOK_EPI_NONE, where it is dy itself and pre is not read):
+ *   dx = dp w + dx_add,  dw = dp^T x + dw_add,  db = sum_m dp  (before that rounding),
+ * each summed in fp32 and rounded once.  dx [M][K], dw [P][K] and db [P] fp32 may be NULL:
+ * that gradient is then not formed (w is read for dx only, x for dw only).  dx_add, dw_add
+ * (of dx's and dw's shape and type) may be NULL and may be the same arrays as dx and dw.
+ * dw and db are written for M = 0 too (dw_add or 0, and 0).  The gradient by res is dy.
+ */
+mok_status mok_linear_backward(const mok_linear_desc* d, const void* dy, const void* pre, const void* x, const void* w,
+                               const void* dx_add, const void* dw_add, void* dx, void* dw, float* db, void* ws,
+                               size_t ws_bytes, void* stream);
 
 /* Static string naming a status code. */
 const char* mok_status_string(mok_status s);

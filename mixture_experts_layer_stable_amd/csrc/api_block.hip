@@ -50,6 +50,41 @@ BalanceArgs balance_args(const mok_balance_desc* d, const float* logits, const i
   return a;
 }
 
+mok_status check_linear(const mok_linear_desc* d) {
+  if (d == nullptr) return MOK_ERR_NULL;
+  if (d->act != MOK_F32 && d->act != MOK_BF16) return MOK_ERR_DTYPE;
+  if (d->epi < MOK_EPI_NONE || d->epi > MOK_EPI_SWIGLU) return MOK_ERR_DTYPE;
+  if (d->reserved != 0 || (d->flags & ~MOK_FLAG_WGRAD_F32) != 0) return MOK_ERR_SHAPE;
+  if (d->M < 0 || d->M >= ((int64_t)1 << 31)) return MOK_ERR_SHAPE;
+  if (d->N < 8 || d->N > (1 << 20) || d->N % 8 != 0) return MOK_ERR_SHAPE;
+  if (d->K < 8 || d->K > (1 << 20) || d->K % 8 != 0) return MOK_ERR_SHAPE;
+  // any array past 2^38 elements is larger than the GPU's memory; output tiles fit 32 bits
+  const int64_t P = d->epi == MOK_EPI_SWIGLU ? 2LL * d->N : d->N;
+  if (std::max<int64_t>(d->M, 1) * std::max<int64_t>(P, d->K) >= (1LL << 38) || P * d->K >= (1LL << 38))
+    return MOK_ERR_SHAPE;
+  return MOK_OK;
+}
+
+int linear_p(const mok_linear_desc* d) { return d->epi == MOK_EPI_SWIGLU ? 2 * d->N : d->N; }
+
+// Backward workspace: dp rows, bias-gradient parts, then the partial products of dx and dw
+// (used one after the other).
+struct LinearBwd {
+  size_t dp, db, part, bytes;
+};
+LinearBwd linear_bwd(const mok_linear_desc* d) {
+  const int P = linear_p(d);
+  LinearBwd w;
+  size_t o = 0;
+  w.dp = o; o = up(o + (d->epi == MOK_EPI_NONE ? 0 : (size_t)elem_size(d->act) * (size_t)d->M * P));
+  w.db = o; o = up(o + 4 * (size_t)linear_db_parts(d->M, d->N) * P);
+  w.part = o;
+  o = up(o + std::max(linear_part_bytes(LIN_DX, d->act, MOK_EPI_NONE, d->M, d->K, P),
+                      linear_part_bytes(LIN_DW, d->act, MOK_EPI_NONE, P, d->K, d->M)));
+  w.bytes = o;
+  return w;
+}
+
 }  // namespace
 
 // A pointer that may be NULL, aligned when it is not.
@@ -204,6 +239,100 @@ mok_status mok_balance_backward(const mok_balance_desc* d, const float* logits, 
   a.dloss = dloss;
   a.dlogits = dlogits;
   MOK_LAUNCH("balance", (hipStream_t)stream, launch_balance_bwd(a, (hipStream_t)stream));
+  return MOK_OK;
+}
+
+mok_status mok_linear_workspace_query(const mok_linear_desc* d, mok_linear_sizes* sizes) {
+  mok_status st = check_linear(d);
+  if (st != MOK_OK) return st;
+  if (sizes == nullptr) return MOK_ERR_NULL;
+  sizes->fwd_ws = up(linear_part_bytes(LIN_FWD, d->act, d->epi, d->M, d->N, d->K));
+  sizes->bwd_ws = linear_bwd(d).bytes;
+  return MOK_OK;
+}
+
+mok_status mok_linear_forward(const mok_linear_desc* d, const void* x, const void* w, const float* bias,
+                              const void* res, void* y, void* pre, void* ws, size_t ws_bytes, void* stream) {
+  mok_linear_sizes sz;
+  mok_status st = mok_linear_workspace_query(d, &sz);
+  if (st != MOK_OK) return st;
+  if ((st = need(ws_bytes, sz.fwd_ws)) != MOK_OK) return st;
+  if (d->M == 0) return MOK_OK;  // empty arrays may be NULL
+  MOK_REQUIRE(x);
+  MOK_REQUIRE(w);
+  MOK_OPTIONAL(bias);
+  MOK_OPTIONAL(res);
+  MOK_REQUIRE(y);
+  MOK_OPTIONAL(pre);
+  if (sz.fwd_ws > 0) MOK_REQUIRE(ws);
+  LinearArgs a{};
+  a.a = x;
+  a.b = w;
+  a.M = d->M;
+  a.N = d->N;
+  a.K = d->K;
+  a.bias = bias;
+  a.add = res;
+  a.out = y;
+  a.pre = pre;
+  a.part = (float*)ws;
+  a.split = linear_split(LIN_FWD, d->act, d->epi, d->M, d->N, d->K);
+  MOK_LAUNCH("linear", (hipStream_t)stream,
+             launch_linear(a, LIN_FWD, d->act, d->epi, d->act == MOK_F32, (hipStream_t)stream));
+  return MOK_OK;
+}
+
+mok_status mok_linear_backward(const mok_linear_desc* d, const void* dy, const void* pre, const void* x, const void* w,
+                               const void* dx_add, const void* dw_add, void* dx, void* dw, float* db, void* ws,
+                               size_t ws_bytes, void* stream) {
+  mok_status st = check_linear(d);
+  if (st != MOK_OK) return st;
+  const LinearBwd L = linear_bwd(d);
+  if ((st = need(ws_bytes, L.bytes)) != MOK_OK) return st;
+  const bool f = d->epi != MOK_EPI_NONE;
+  MOK_OPTIONAL(dx_add);
+  MOK_OPTIONAL(dw_add);
+  MOK_OPTIONAL(dx);
+  MOK_OPTIONAL(dw);
+  MOK_OPTIONAL(db);
+  if (d->M > 0) {
+    MOK_REQUIRE(dy);
+    if (f) MOK_REQUIRE(pre);
+    if (dx != nullptr) MOK_REQUIRE(w);
+    if (dw != nullptr) MOK_REQUIRE(x);
+  }
+  if (L.bytes > 0) MOK_REQUIRE(ws);
+  const int P = linear_p(d);
+  const hipStream_t s = (hipStream_t)stream;
+  char* wb = (char*)ws;
+  const void* dp = f ? wb + L.dp : dy;
+  float* dbp = db != nullptr ? (float*)(wb + L.db) : nullptr;
+  if (d->M > 0 && ((f && (dx != nullptr || dw != nullptr)) || db != nullptr))
+    MOK_LAUNCH("linear", s, launch_linear_dpre(dy, pre, d->M, d->N, d->act, d->epi, f ? wb + L.dp : nullptr, dbp, s));
+  if (db != nullptr) MOK_LAUNCH("linear", s, launch_col_sum(dbp, linear_db_parts(d->M, d->N), P, db, true, s));
+  LinearArgs a{};
+  a.a = dp;
+  a.N = d->K;
+  a.part = (float*)(wb + L.part);
+  if (dx != nullptr && d->M > 0) {
+    a.b = w;
+    a.M = d->M;
+    a.K = P;
+    a.add = dx_add;
+    a.out = dx;
+    a.split = linear_split(LIN_DX, d->act, MOK_EPI_NONE, a.M, a.N, a.K);
+    MOK_LAUNCH("linear", s, launch_linear(a, LIN_DX, d->act, MOK_EPI_NONE, d->act == MOK_F32, s));
+  }
+  if (dw != nullptr) {
+    a.b = x;
+    a.M = P;
+    a.K = d->M;
+    a.add = dw_add;
+    a.out = dw;
+    a.split = linear_split(LIN_DW, d->act, MOK_EPI_NONE, a.M, a.N, a.K);
+    MOK_LAUNCH("linear", s, launch_linear(a, LIN_DW, d->act, MOK_EPI_NONE,
+                                          d->act == MOK_F32 || (d->flags & MOK_FLAG_WGRAD_F32) != 0, s));
+  }
   return MOK_OK;
 }
 

@@ -1,5 +1,5 @@
 // Launch interface between the C-ABI layer (api_block.hip) and the operators around the
-// layer step (norm.hip, balance.hip).
+// layer step (norm.hip, balance.hip, linear.hip).
 #pragma once
 #include "common.h"
 
@@ -65,5 +65,36 @@ struct BalanceArgs {
 };
 hipError_t launch_balance_fwd(const BalanceArgs& a, hipStream_t s);
 hipError_t launch_balance_bwd(const BalanceArgs& a, hipStream_t s);
+
+// ---- matrix product with epilogue ----
+enum LinearKind { LIN_FWD = 0, LIN_DX = 1, LIN_DW = 2 };
+
+// out[m][n] = sum_k A(m, k) B(n, k), m < M, n < N, k < K; ld in elements.
+//   LIN_FWD  A = x rows, B = w rows (both K-contiguous); N counts the outputs y has; with
+//            SWIGLU, B has 2N rows
+//   LIN_DX   A = dp rows (K-contiguous), B(n, k) = w[k][n]
+//   LIN_DW   A(m, k) = dp[k][m], B(n, k) = x[k][n]
+struct LinearArgs {
+  const void* a;
+  const void* b;
+  int64_t M, K;
+  int N;
+  const float* bias;  // LIN_FWD
+  const void* add;    // [M][N] added to the result, or nullptr
+  void* out;          // [M][N]
+  void* pre;          // LIN_FWD: [M][P], or nullptr
+  float* part;        // partial products of a split K: [split][M][P] fp32
+  int split;
+};
+// Slices of K (workspace: linear_part_bytes); a function of the shape and type only.
+int linear_split(int kind, int act, int epi, int64_t M, int N, int64_t K);
+size_t linear_part_bytes(int kind, int act, int epi, int64_t M, int N, int64_t K);
+hipError_t launch_linear(const LinearArgs& a, int kind, int act, int epi, bool out_f32, hipStream_t s);
+
+// dp = dy f'(pre) (epi != NONE; dp may be nullptr with NONE) and the column sums' parts
+// [linear_db_parts][P] fp32 (nullptr: not formed)
+int linear_db_parts(int64_t M, int N);
+hipError_t launch_linear_dpre(const void* dy, const void* pre, int64_t M, int N, int act, int epi, void* dp, float* part,
+                              hipStream_t s);
 
 }  // namespace mok

@@ -1,0 +1,236 @@
+// Matrix product with bias, activation and residual in its epilogue, forward and backward.
+#include "linear.h"
+
+namespace mok {
+
+namespace {
+
+// K-contiguous operand rows with a ragged K: 16-byte chunks at or past K read as zeros.
+template <typename T, int ROWS>
+struct KTailStager {
+  static constexpr int VE = Elem<T>::VE;
+  static constexpr int BKE = kRowBytes / (int)sizeof(T);
+  static constexpr int NV = ROWS * 8 / kThreads;
+  const T* ptr[NV];
+  uint4 r[NV];
+  int64_t K;
+  int tid;
+  // rowptr(row): start of the row, or nullptr for a row of zeros
+  template <class F> __device__ __forceinline__ void init(int tid_, int64_t K_, F rowptr) {
+    tid = tid_;
+    K = K_;
+#pragma unroll
+    for (int v = 0; v < NV; ++v) ptr[v] = rowptr((tid + v * kThreads) >> 3);
+  }
+  __device__ __forceinline__ void load(int kt) {
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      const int64_t k = (int64_t)kt * BKE + ((tid + v * kThreads) & 7) * VE;
+      r[v] = ptr[v] != nullptr && k < K ? ldg16(ptr[v] + k) : make_uint4(0, 0, 0, 0);
+    }
+  }
+  __device__ __forceinline__ void store(char* lds) const {
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      const int i = tid + v * kThreads;
+      *reinterpret_cast<uint4*>(lds + lds_off(i >> 3, i & 7)) = r[v];
+    }
+  }
+};
+
+// MN-contiguous operand: element (k, mn) at base[k * ld + mn], zeros outside.
+template <typename T>
+struct MnSource {
+  const T* base;
+  int64_t ld, K, MN, mn0;
+  __device__ __forceinline__ uint4 operator()(int64_t k, int mn) const {
+    return k < K && mn0 + mn < MN ? ldg16(base + k * ld + mn0 + mn) : make_uint4(0, 0, 0, 0);
+  }
+};
+
+using Tile = Tiling<128, 128, 2, 2>;
+
+// One 128x128 tile per workgroup: operands staged through registers into a double-buffered
+// LDS tile (gemm.h), right for every shape and type.
+template <typename T, int KIND, int EPI, typename TO>
+__global__ __launch_bounds__(256) void linear_simple_kernel(LinearArgs a) {
+  __shared__ __align__(1024) char smem[Tile::LDS_BYTES];
+  constexpr bool SW = EPI == MOK_EPI_SWIGLU;
+  constexpr int BKE = kRowBytes / (int)sizeof(T);
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, wm = wave >> 1, wn = wave & 1;
+  constexpr int BN = SW ? Tile::BN / 2 : Tile::BN;  // outputs of a tile's columns
+  const int NT = (a.N + BN - 1) / BN;
+  const int64_t m0 = (int64_t)(blockIdx.x / NT) * Tile::BM;
+  const int n0 = (blockIdx.x % NT) * BN;
+  const int KT = (int)((a.K + BKE - 1) / BKE);
+  f32x16_t acc[Tile::FM][Tile::FN];
+  const T* A = (const T*)a.a;
+  const T* B = (const T*)a.b;
+  // first output column of tile column j (SWIGLU: 32-column blocks of gate and up in turn)
+  const auto col = [&](int j) { return SW ? n0 + (j / Tile::WTN) * (Tile::WTN / 2) + (j & 31) : n0 + j; };
+  if constexpr (KIND == LIN_FWD) {
+    KTailStager<T, Tile::BM> sa;
+    sa.init(tid, a.K, [&](int r) { return m0 + r < a.M ? A + (m0 + r) * a.K : nullptr; });
+    KTailStager<T, Tile::BN> sb;
+    sb.init(tid, a.K, [&](int j) -> const T* {
+      const int c = col(j);
+      if (c >= a.N) return nullptr;
+      return B + (int64_t)(SW && (j & 32) ? a.N + c : c) * a.K;
+    });
+    main_loop<T, Tile>(sa, sb, KT, smem, wm, wn, lane, acc);
+  } else if constexpr (KIND == LIN_DX) {
+    KTailStager<T, Tile::BM> sa;
+    sa.init(tid, a.K, [&](int r) { return m0 + r < a.M ? A + (m0 + r) * a.K : nullptr; });
+    MNStager<T, Tile::BN, MnSource<T>> sb;
+    sb.tid = tid;
+    sb.src = MnSource<T>{B, a.N, a.K, a.N, n0};
+    main_loop<T, Tile>(sa, sb, KT, smem, wm, wn, lane, acc);
+  } else {
+    MNStager<T, Tile::BM, MnSource<T>> sa;
+    sa.tid = tid;
+    sa.src = MnSource<T>{A, a.M, a.K, a.M, m0};
+    MNStager<T, Tile::BN, MnSource<T>> sb;
+    sb.tid = tid;
+    sb.src = MnSource<T>{B, a.N, a.K, a.N, n0};
+    main_loop<T, Tile>(sa, sb, KT, smem, wm, wn, lane, acc);
+  }
+  __syncthreads();
+  epilogue16<Tile, SW>(acc, smem, wave, wm, wn, lane,
+                       [&](int row, int j, const float (&g)[16], const float (&u)[16]) {
+    const int64_t m = m0 + row;
+    if (m >= a.M) return;
+    const int c = col(j);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      if (c + 8 * h >= a.N) continue;
+      float g8[8], u8[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        g8[i] = g[8 * h + i];
+        u8[i] = SW ? u[8 * h + i] : 0.0f;
+      }
+      linear_store8<KIND, EPI, TO, T>(a, m, c + 8 * h, g8, u8);
+    }
+  });
+}
+
+template <typename T, int KIND, int EPI, typename TO>
+void run_simple(const LinearArgs& a, hipStream_t s) {
+  const int bn = EPI == MOK_EPI_SWIGLU ? Tile::BN / 2 : Tile::BN;
+  const dim3 grid((unsigned)(((a.N + bn - 1) / bn) * ((a.M + Tile::BM - 1) / Tile::BM)));
+  hipLaunchKernelGGL((linear_simple_kernel<T, KIND, EPI, TO>), grid, dim3(256), 0, s, a);
+}
+
+template <typename T>
+void run_kind(const LinearArgs& a, int kind, int epi, bool out_f32, hipStream_t s) {
+  if (kind == LIN_FWD) {
+    if (epi == MOK_EPI_NONE) run_simple<T, LIN_FWD, MOK_EPI_NONE, T>(a, s);
+    else if (epi == MOK_EPI_SILU) run_simple<T, LIN_FWD, MOK_EPI_SILU, T>(a, s);
+    else if (epi == MOK_EPI_GELU) run_simple<T, LIN_FWD, MOK_EPI_GELU, T>(a, s);
+    else run_simple<T, LIN_FWD, MOK_EPI_SWIGLU, T>(a, s);
+  } else if (kind == LIN_DX) {
+    run_simple<T, LIN_DX, MOK_EPI_NONE, T>(a, s);
+  } else if (out_f32) {
+    run_simple<T, LIN_DW, MOK_EPI_NONE, float>(a, s);
+  } else {
+    run_simple<T, LIN_DW, MOK_EPI_NONE, T>(a, s);
+  }
+}
+
+// ---- dp = dy f'(pre), and the parts of the bias gradient ----
+// A thread keeps eight columns of dp and walks down the rows of its part; each input is read
+// once and dp written once (HBM-bound).
+constexpr int kDpreRows = 64;  // rows of a part, at least
+
+template <typename T, int EPI>
+__global__ __launch_bounds__(256) void linear_dpre_kernel(const T* __restrict__ dy, const T* __restrict__ pre,
+                                                          int64_t M, int N, int64_t rows, T* __restrict__ dp,
+                                                          float* __restrict__ part) {
+  constexpr bool SW = EPI == MOK_EPI_SWIGLU;
+  const int c = (blockIdx.x * 256 + threadIdx.x) * 8, P = SW ? 2 * N : N;
+  if (c >= N) return;
+  const int64_t m0 = (int64_t)blockIdx.y * rows, m1 = min(M, m0 + rows);
+  float sg[8], su[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) sg[i] = su[i] = 0.0f;
+  for (int64_t m = m0; m < m1; ++m) {
+    float d[8], p[8], u[8];
+    load8(dy + m * N + c, d);
+    if constexpr (EPI != MOK_EPI_NONE) load8(pre + m * P + c, p);
+    if constexpr (SW) load8(pre + m * P + N + c, u);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      if constexpr (EPI == MOK_EPI_SILU || SW) {
+        const float s = sigmoid_f(p[i]), f = s * (1.0f + p[i] * (1.0f - s));
+        if constexpr (SW) {
+          const float up = d[i] * p[i] * s;
+          d[i] *= u[i] * f;
+          u[i] = up;
+        } else {
+          d[i] *= f;
+        }
+      } else if constexpr (EPI == MOK_EPI_GELU) {
+        d[i] *= phi_f(p[i]) + p[i] * 0.39894228040143268f * expf(-0.5f * p[i] * p[i]);
+      }
+      sg[i] += d[i];
+      if constexpr (SW) su[i] += u[i];
+    }
+    if constexpr (EPI != MOK_EPI_NONE) store8(dp + m * P + c, d);
+    if constexpr (SW) store8(dp + m * P + N + c, u);
+  }
+  if (part == nullptr) return;
+  float* o = part + (int64_t)blockIdx.y * P + c;
+  store8(o, sg);
+  if constexpr (SW) store8(o + N, su);
+}
+
+// Rows of a part: the M rows go to about 2048 workgroups' worth of (256 x 8 columns, part).
+int64_t dpre_rows(int64_t M, int N) {
+  const int64_t cols = (N + 2047) / 2048, parts = std::max<int64_t>(1, 2048 / cols);
+  return std::max<int64_t>(kDpreRows, (M + parts - 1) / parts);
+}
+
+template <typename T>
+void run_dpre(const void* dy, const void* pre, int64_t M, int N, int epi, void* dp, float* part, hipStream_t s) {
+  const int64_t rows = dpre_rows(M, N);
+  const dim3 grid((N + 2047) / 2048, (unsigned)((M + rows - 1) / rows)), block(256);
+  const T *d = (const T*)dy, *p = (const T*)pre;
+  if (epi == MOK_EPI_NONE)
+    hipLaunchKernelGGL((linear_dpre_kernel<T, MOK_EPI_NONE>), grid, block, 0, s, d, p, M, N, rows, (T*)dp, part);
+  else if (epi == MOK_EPI_SILU)
+    hipLaunchKernelGGL((linear_dpre_kernel<T, MOK_EPI_SILU>), grid, block, 0, s, d, p, M, N, rows, (T*)dp, part);
+  else if (epi == MOK_EPI_GELU)
+    hipLaunchKernelGGL((linear_dpre_kernel<T, MOK_EPI_GELU>), grid, block, 0, s, d, p, M, N, rows, (T*)dp, part);
+  else
+    hipLaunchKernelGGL((linear_dpre_kernel<T, MOK_EPI_SWIGLU>), grid, block, 0, s, d, p, M, N, rows, (T*)dp, part);
+}
+
+}  // namespace
+
+int linear_split(int, int, int, int64_t, int, int64_t) { return 1; }
+
+size_t linear_part_bytes(int kind, int act, int epi, int64_t M, int N, int64_t K) {
+  const int split = linear_split(kind, act, epi, M, N, K);
+  return split > 1 ? 4 * (size_t)split * (size_t)M * (epi == MOK_EPI_SWIGLU ? 2 * N : N) : 0;
+}
+
+hipError_t launch_linear(const LinearArgs& a, int kind, int act, int epi, bool out_f32, hipStream_t s) {
+  if (act == MOK_F32) run_kind<float>(a, kind, epi, out_f32, s);
+  else run_kind<bf16>(a, kind, epi, out_f32, s);
+  return hipGetLastError();
+}
+
+int linear_db_parts(int64_t M, int N) {
+  if (M == 0) return 0;
+  const int64_t rows = dpre_rows(M, N);
+  return (int)((M + rows - 1) / rows);
+}
+
+hipError_t launch_linear_dpre(const void* dy, const void* pre, int64_t M, int N, int act, int epi, void* dp, float* part,
+                              hipStream_t s) {
+  if (act == MOK_F32) run_dpre<float>(dy, pre, M, N, epi, dp, part, s);
+  else run_dpre<bf16>(dy, pre, M, N, epi, dp, part, s);
+  return hipGetLastError();
+}
+
+}  // namespace mok

@@ -23,6 +23,8 @@ FLAG_WGRAD_DEFER = 2
 FLAG_REPLAY = 4
 FLAG_FUSED = 8
 FLAG_X_QUANT = 16
+EPI_NONE, EPI_SILU, EPI_GELU, EPI_SWIGLU = 0, 1, 2, 3
+EPILOGUES = {"none": EPI_NONE, "silu": EPI_SILU, "gelu": EPI_GELU, "swiglu": EPI_SWIGLU}
 SCORE_SOFTMAX, SCORE_SIGMOID = 0, 1
 SCORES = {"softmax": SCORE_SOFTMAX, "sigmoid": SCORE_SIGMOID}
 DTYPES = {"f32": F32, "bf16": BF16, "mxfp8": MXFP8, "mxfp4": MXFP4}
@@ -90,6 +92,15 @@ class _BalanceDesc(ctypes.Structure):
                 ("zcoef", ctypes.c_float), ("reserved", ctypes.c_int32)]
 
 
+class _LinearDesc(ctypes.Structure):
+    _fields_ = [("M", ctypes.c_int64), ("N", ctypes.c_int32), ("K", ctypes.c_int32), ("act", ctypes.c_int32),
+                ("epi", ctypes.c_int32), ("flags", ctypes.c_uint32), ("reserved", ctypes.c_int32)]
+
+
+class _LinearSizes(ctypes.Structure):
+    _fields_ = [("fwd_ws", ctypes.c_size_t), ("bwd_ws", ctypes.c_size_t)]
+
+
 MX_LAYOUT_FIELDS = ("fwd_slot", "xq", "xs", "hq", "hs", "bwd_slot", "dyq", "dys", "dguq", "dgus", "st_xs", "st_dos",
                     "st_h", "st_dgu", "pofs", "dot", "dots", "ht", "hts", "dgut", "dguts", "xt", "xts")
 
@@ -124,6 +135,9 @@ def _load():
         "mok_balance_workspace_query": [ctypes.POINTER(_BalanceDesc), ctypes.POINTER(Z)],
         "mok_balance_forward": [ctypes.POINTER(_BalanceDesc)] + [P] * 10 + [Z, P],
         "mok_balance_backward": [ctypes.POINTER(_BalanceDesc)] + [P] * 9,
+        "mok_linear_workspace_query": [ctypes.POINTER(_LinearDesc), ctypes.POINTER(_LinearSizes)],
+        "mok_linear_forward": [ctypes.POINTER(_LinearDesc)] + [P] * 7 + [Z, P],
+        "mok_linear_backward": [ctypes.POINTER(_LinearDesc)] + [P] * 10 + [Z, P],
     }
     for name, args in sig.items():
         f = getattr(lib, name)
@@ -142,7 +156,8 @@ EXPORTS = ("mok_workspace_query", "mok_schedule_layout_query", "mok_saved_layout
            "mok_schedule_build", "mok_moe_forward", "mok_moe_forward_noalloc", "mok_moe_backward",
            "mok_weights_quantize", "mok_status_string", "mok_version", "mok_trace_bind",
            "mok_norm_workspace_query", "mok_rmsnorm_forward", "mok_rmsnorm_backward",
-           "mok_balance_workspace_query", "mok_balance_forward", "mok_balance_backward")
+           "mok_balance_workspace_query", "mok_balance_forward", "mok_balance_backward",
+           "mok_linear_workspace_query", "mok_linear_forward", "mok_linear_backward")
 NOALLOC_WS_BYTES = 32 << 20
 
 
@@ -478,6 +493,59 @@ def balance_backward(d: BalanceDesc, logits, counts, tokens, stat, dloss, dlogit
          _ptr("counts", counts, i32, (S, E), dev), _ptr("tokens", tokens, i32, (S + 2,), dev),
          _ptr("stat", stat, f32, (T,), dev), _ptr("dloss", dloss, f32, (2,), dev),
          _ptr("dlogits", dlogits, TORCH_DTYPE.get(d.grad), (T, E), dev))
+
+
+@dataclass(frozen=True)
+class LinearDesc:
+    """y = f(x w^T + bias) + res with x [M, K] and y [M, N] (mok_linear_desc)."""
+    M: int
+    N: int
+    K: int
+    act: int = BF16
+    epi: int = EPI_NONE
+    flags: int = 0
+
+    def __post_init__(self):
+        object.__setattr__(self, "_c", _LinearDesc(self.M, self.N, self.K, self.act, self.epi, self.flags, 0))
+
+    def c(self) -> _LinearDesc:
+        return self._c
+
+    @property
+    def P(self) -> int:
+        """Columns of the product (rows of w)."""
+        return 2 * self.N if self.epi == EPI_SWIGLU else self.N
+
+
+def linear_workspace_query(d: LinearDesc) -> dict:
+    s = _LinearSizes()
+    _check(_lib.mok_linear_workspace_query(d._c, s), "mok_linear_workspace_query")
+    return dict(fwd_ws=s.fwd_ws, bwd_ws=s.bwd_ws)
+
+
+def linear_forward(d: LinearDesc, x, w, y, bias=None, res=None, pre=None, ws=None, stream=None):
+    """pre = x w^T + bias; y = f(pre) + res."""
+    M, N, K, P, t, dev = d.M, d.N, d.K, d.P, TORCH_DTYPE.get(d.act), x.device
+    wp, wn = _ws(ws, dev)
+    _run(_lib.mok_linear_forward, "mok_linear_forward", dev, stream, d._c, _ptr("x", x, t, (M, K), dev),
+         _ptr("w", w, t, (P, K), dev), _ptr("bias", bias, torch.float32, (P,), dev, True),
+         _ptr("res", res, t, (M, N), dev, True), _ptr("y", y, t, (M, N), dev), _ptr("pre", pre, t, (M, P), dev, True),
+         wp, wn)
+
+
+def linear_backward(d: LinearDesc, dy, x, w, dx=None, dw=None, db=None, pre=None, dx_add=None, dw_add=None, ws=None,
+                    stream=None):
+    """dp = dy f'(pre); dx = dp w + dx_add, dw = dp^T x + dw_add, db = sum dp (each only when its tensor is given)."""
+    M, N, K, P, t, dev = d.M, d.N, d.K, d.P, TORCH_DTYPE.get(d.act), dy.device
+    wt = torch.float32 if d.flags & FLAG_WGRAD_F32 else t
+    if (dx_add is not None and dx is None) or (dw_add is not None and dw is None):
+        raise ValueError("dx_add, dw_add: without the gradient that they are added to")
+    wp, wn = _ws(ws, dev)
+    _run(_lib.mok_linear_backward, "mok_linear_backward", dev, stream, d._c, _ptr("dy", dy, t, (M, N), dev),
+         _ptr("pre", pre, t, (M, P), dev, d.epi == EPI_NONE), _ptr("x", x, t, (M, K), dev, dw is None),
+         _ptr("w", w, t, (P, K), dev, dx is None), _ptr("dx_add", dx_add, t, (M, K), dev, True),
+         _ptr("dw_add", dw_add, wt, (P, K), dev, True), _ptr("dx", dx, t, (M, K), dev, True),
+         _ptr("dw", dw, wt, (P, K), dev, True), _ptr("db", db, torch.float32, (P,), dev, True), wp, wn)
 
 
 class KernelTrace:
