@@ -215,8 +215,8 @@ size_t linear_part_bytes(int kind, int act, int epi, int64_t M, int N, int64_t K
 }
 
 hipError_t launch_linear(const LinearArgs& a, int kind, int act, int epi, bool out_f32, hipStream_t s) {
-  if (act == MOK_F32) run_kind<float>(a, kind, epi, out_f32, s);
-  else run_kind<bf16>(a, kind, epi, out_f32, s);
+  if (act == MOK_BF16) return launch_linear_bf16(a, kind, epi, out_f32, s);
+  run_kind<float>(a, kind, epi, out_f32, s);
   return hipGetLastError();
 }
 
