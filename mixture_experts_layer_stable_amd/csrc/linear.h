@@ -19,59 +19,96 @@ __device__ __forceinline__ void load8(const T* p, float (&v)[8]) {
     for (int i = 0; i < 4; ++i) { v[i] = a[i]; v[4 + i] = b[i]; }
   }
 }
-template <typename T>
+// NT: a non-temporal store, for outputs that no cache would keep anyway.
+template <bool NT>
+__device__ __forceinline__ void put16(void* p, const uint4& v) {
+  typedef unsigned int u32x4_t __attribute__((ext_vector_type(4)));
+  if constexpr (NT) __builtin_nontemporal_store(u32x4_t{v.x, v.y, v.z, v.w}, reinterpret_cast<u32x4_t*>(p));
+  else stg16(p, v);
+}
+template <bool NT = false, typename T>
 __device__ __forceinline__ void store8(T* p, const float (&v)[8]) {
   if constexpr (std::is_same<T, bf16>::value) {
-    stg16(p, pack(v, (bf16*)nullptr));
+    put16<NT>(p, pack(v, (bf16*)nullptr));
   } else {
     float a[4], b[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) { a[i] = v[i]; b[i] = v[4 + i]; }
-    stg16(p, pack(a, (float*)nullptr));
-    stg16(p + 4, pack(b, (float*)nullptr));
+    put16<NT>(p, pack(a, (float*)nullptr));
+    put16<NT>(p + 4, pack(b, (float*)nullptr));
   }
 }
 
 __device__ __forceinline__ float sigmoid_f(float z) { return 1.0f / (1.0f + expf(-z)); }
+// The same to 2^-20 by the hardware's exp2 and reciprocal, for results that are rounded to bf16:
+// a wave that has its SIMD to itself waits for every instruction of an epilogue (16384 x (2 x 2048)
+// x 7168 SWIGLU: 10 us less).
+__device__ __forceinline__ float sigmoid_fast(float z) {
+  return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(z * -1.44269504088896341f));
+}
 __device__ __forceinline__ float phi_f(float z) { return 0.5f * erfcf(z * -0.70710678118654752f); }
 
-// Columns c .. c+7 (c a multiple of 8, in range) of row m: g = the products, u = those of the
-// up columns (SWIGLU only). T: type of add, out; TP: of pre.
-template <int KIND, int EPI, typename T, typename TP>
-__device__ __forceinline__ void linear_store8(const LinearArgs& a, int64_t m, int c, float (&g)[8], float (&u)[8]) {
+// What is added to columns c .. c+7 of row m, as it lies in memory (zeros without an addend).
+template <typename T>
+struct Raw8 {
+  uint4 v[std::is_same<T, bf16>::value ? 1 : 2];
+};
+template <typename T>
+__device__ __forceinline__ Raw8<T> linear_add8(const LinearArgs& a, int64_t m, int c) {
+  Raw8<T> r;
+#pragma unroll
+  for (auto& v : r.v) v = make_uint4(0, 0, 0, 0);
+  if (a.add != nullptr) {
+    const T* p = (const T*)a.add + m * a.N + c;
+    r.v[0] = ldg16(p);
+    if constexpr (!std::is_same<T, bf16>::value) r.v[1] = ldg16(p + 4);
+  }
+  return r;
+}
+
+// Columns c .. c+7 (c a multiple of 8, in range) of row m: g = the products and bias, u = those of
+// the up columns (SWIGLU only), add = linear_add8's. T: type of add, out; TP: of pre. NT:
+// non-temporal stores.
+template <int KIND, int EPI, typename T, typename TP, bool NT = false>
+__device__ __forceinline__ void linear_store8(const LinearArgs& a, int64_t m, int c, float (&g)[8], float (&u)[8],
+                                              const Raw8<T>& add) {
   if constexpr (KIND == LIN_FWD) {
     const int P = EPI == MOK_EPI_SWIGLU ? 2 * a.N : a.N;
-    if (a.bias != nullptr) {
-      float b[8];
-      load8(a.bias + c, b);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) g[i] += b[i];
-      if constexpr (EPI == MOK_EPI_SWIGLU) {
-        load8(a.bias + a.N + c, b);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) u[i] += b[i];
-      }
-    }
     if (a.pre != nullptr) {
       TP* p = (TP*)a.pre + m * P + c;
-      store8(p, g);
-      if constexpr (EPI == MOK_EPI_SWIGLU) store8(p + a.N, u);
+      store8<NT>(p, g);
+      if constexpr (EPI == MOK_EPI_SWIGLU) store8<NT>(p + a.N, u);
     }
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      if constexpr (EPI == MOK_EPI_SILU) g[i] *= sigmoid_f(g[i]);
+      if constexpr (EPI == MOK_EPI_SILU || EPI == MOK_EPI_SWIGLU)
+        g[i] *= std::is_same<T, bf16>::value ? sigmoid_fast(g[i]) : sigmoid_f(g[i]);
+      if constexpr (EPI == MOK_EPI_SWIGLU) g[i] *= u[i];
       if constexpr (EPI == MOK_EPI_GELU) g[i] *= phi_f(g[i]);
-      if constexpr (EPI == MOK_EPI_SWIGLU) g[i] *= sigmoid_f(g[i]) * u[i];
     }
   }
-  const int64_t o = m * a.N + c;
   if (a.add != nullptr) {
     float r[8];
-    load8((const T*)a.add + o, r);
+    load8(reinterpret_cast<const T*>(&add.v[0]), r);
 #pragma unroll
     for (int i = 0; i < 8; ++i) g[i] += r[i];
   }
-  store8((T*)a.out + o, g);
+  store8<NT>((T*)a.out + m * a.N + c, g);
+}
+
+// g += bias of columns c .. c+7 (u: of the up columns)
+template <int EPI>
+__device__ __forceinline__ void linear_bias8(const LinearArgs& a, int c, float (&g)[8], float (&u)[8]) {
+  if (a.bias == nullptr) return;
+  float b[8];
+  load8(a.bias + c, b);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) g[i] += b[i];
+  if constexpr (EPI == MOK_EPI_SWIGLU) {
+    load8(a.bias + a.N + c, b);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) u[i] += b[i];
+  }
 }
 
 }  // namespace mok

@@ -109,7 +109,8 @@ __global__ __launch_bounds__(256) void linear_simple_kernel(LinearArgs a) {
         g8[i] = g[8 * h + i];
         u8[i] = SW ? u[8 * h + i] : 0.0f;
       }
-      linear_store8<KIND, EPI, TO, T>(a, m, c + 8 * h, g8, u8);
+      if constexpr (KIND == LIN_FWD) linear_bias8<EPI>(a, c + 8 * h, g8, u8);
+      linear_store8<KIND, EPI, TO, T>(a, m, c + 8 * h, g8, u8, linear_add8<TO>(a, m, c + 8 * h));
     }
   });
 }
@@ -140,7 +141,7 @@ void run_kind(const LinearArgs& a, int kind, int epi, bool out_f32, hipStream_t 
 // ---- dp = dy f'(pre), and the parts of the bias gradient ----
 // A thread keeps eight columns of dp and walks down the rows of its part; each input is read
 // once and dp written once (HBM-bound).
-constexpr int kDpreRows = 64;  // rows of a part, at least
+constexpr int kDpreRows = 16;  // rows of a part, at least: its fp32 sums then stay an eighth of what is read
 
 template <typename T, int EPI>
 __global__ __launch_bounds__(256) void linear_dpre_kernel(const T* __restrict__ dy, const T* __restrict__ pre,
@@ -153,6 +154,7 @@ __global__ __launch_bounds__(256) void linear_dpre_kernel(const T* __restrict__ 
   float sg[8], su[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) sg[i] = su[i] = 0.0f;
+#pragma unroll 4
   for (int64_t m = m0; m < m1; ++m) {
     float d[8], p[8], u[8];
     load8(dy + m * N + c, d);

@@ -1,33 +1,40 @@
 // bf16 matrix product on direct global->LDS loads, for the products of linear.hip.
 //
-// A workgroup multiplies one BM x BN tile; both operands of a 64-element K-tile arrive in one
-// of two LDS stages by global_load_lds_dwordx4 (gemm2.h's tile layouts, with ragged edges).
-// A fragment is read one 16-k step ahead of its MFMAs, across the stage change too: at the last
-// step of a K-tile a wave holds all fragments it still needs, so the barrier there frees the
-// stage for K-tile kt+2's loads while the step's MFMAs still run, and those cover the first
-// fragment reads of K-tile kt+1.
+// A workgroup of four waves multiplies one BM x BN tile, a wave a quarter of it; both operands
+// of a 64-element K-tile arrive in one of two LDS stages by global_load_lds_dwordx4 (gemm2.h's
+// tile layouts, with ragged edges). With 256 x 256 tiles a SIMD holds one wave (256 fp32
+// accumulators per lane), so nothing but the order of its own instructions hides its loads: every
+// LDS read and DMA of the loop has its place between two MFMAs (see dense_tile).
 #pragma once
 #include "gemm2.h"
 #include "linear.h"
 
 namespace mok {
 
+// LDS byte offset of a shared array (wave-uniform).
+__device__ __forceinline__ uint32_t lds_offset(const char* p) {
+  return __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(lds_void_t)p);
+}
+
+__device__ __forceinline__ void dma16_at(const char* sbase, uint32_t voff, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(lds), "v"(voff), "s"(sbase) : "memory", "m0");
+}
+
 static __device__ uint4 g_zero_16 = {};  // what is read past the end of K
 
 // K-contiguous operand: tile row r starts at sbase + voff(r); K-tile kt is its bytes
-// 128 kt .. +127, chunks at or past K read the zero block.
+// 128 kt .. +127, chunks at or past K read zeros.
 // SW: 32-row blocks of the tile come in turn from the rows at sbase and from those at sbase + up
-// (gate and up rows of w); an instruction's 8 rows lie in one block.
+// (gate and up rows of w); a DMA instruction's 8 rows lie in one block.
 template <int ROWS, int NF, int NW, bool SW = false>
 struct DenseK {
   static constexpr int BYTES = ROWS * 128;
   static constexpr int NI = ROWS / (8 * NW);  // DMA instructions per wave per stage (8 rows each)
   static_assert(ROWS % (8 * NW) == 0, "rows");
   const char* sbase;
+  int64_t up, kbytes;  // kbytes = 2 K
   uint32_t voff[NI];
   uint32_t foff[NF][4];
-  int64_t kbytes;  // 2 K
-  int64_t up;
 
   // rowoff(row): byte offset of the row from its base (below 4 GiB); frow(f): first tile row of
   // fragment f.
@@ -48,25 +55,32 @@ struct DenseK {
       for (int ks = 0; ks < 4; ++ks) foff[f][ks] = row * 128 + 16 * ((2 * ks + (lane >> 5)) ^ swz_k(row));
     }
   }
+  __device__ __forceinline__ int64_t full() const { return kbytes / 128; }  // K-tiles that have all of their K
   __device__ __forceinline__ const char* base(int64_t kt, int j, int wave) const {
     const char* b = sbase + kt * 128;
     if constexpr (SW) b += ((wave + NW * j) >> 2) & 1 ? up : 0;
     return b;
   }
-  __device__ __forceinline__ void issue(int64_t kt, char* stage, int wave) const {
-    if ((kt + 1) * 128 <= kbytes) {
+  // DMA instructions j0 .. j1-1 of K-tile kt into the stage at LDS offset lds; FULL: kt < full()
+  template <bool FULL>
+  __device__ __forceinline__ void issue(int64_t kt, uint32_t lds, int wave, int j0 = 0, int j1 = NI) const {
+    if (FULL || (kt + 1) * 128 <= kbytes) {
 #pragma unroll
-      for (int j = 0; j < NI; ++j) dma16_sv(uniform_ptr(base(kt, j, wave)), voff[j], stage + (wave + NW * j) * 1024);
+      for (int j = j0; j < j1; ++j) dma16_at(uniform_ptr(base(kt, j, wave)), voff[j], lds + (wave + NW * j) * 1024);
     } else {
       const int lane = threadIdx.x & 63;
 #pragma unroll
-      for (int j = 0; j < NI; ++j) {
+      for (int j = j0; j < j1; ++j) {
         const int row = 8 * (wave + NW * j) + (lane >> 3);
         const int ch = (lane & 7) ^ swz_k(row);
-        const char* p = kt * 128 + 16 * ch < kbytes ? base(kt, j, wave) + voff[j] : reinterpret_cast<const char*>(&g_zero_16);
-        dma16(p, stage + (wave + NW * j) * 1024);
+        const char* p = kt * 128 + 16 * ch < kbytes ? base(kt, j, wave) + voff[j]
+                                                    : reinterpret_cast<const char*>(&g_zero_16);
+        dma16_any(p, lds + (wave + NW * j) * 1024);
       }
     }
+  }
+  __device__ __forceinline__ static void dma16_any(const char* p, uint32_t lds) {
+    asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(lds), "v"(p) : "memory", "m0");
   }
   __device__ __forceinline__ uint4 frag(const char* stage, int f, int ks) const {
     return *reinterpret_cast<const uint4*>(stage + foff[f][ks]);
@@ -74,8 +88,8 @@ struct DenseK {
 };
 
 // MN-contiguous operand: k-row k of the tile starts at sbase + k * ld bytes; 64 k-rows x ROWS
-// bf16 per stage. Rows at or past K read the zero block, 16-byte column chunks at or past
-// `cols` read the row's first chunk (their results are not stored).
+// bf16 per stage. Rows at or past K read zeros, 16-byte column chunks at or past `cols` read the
+// row's first chunk (their results are not stored).
 template <int ROWS, int NF, int NW>
 struct DenseMN {
   static constexpr int PITCH = ROWS * 2;
@@ -107,19 +121,20 @@ struct DenseMN {
       foff[f] = k0 * PITCH + 16 * ((mn >> 3) ^ swz_mn(k0)) + 2 * (mn & 7);
     }
   }
-  __device__ __forceinline__ void issue(int64_t kt, char* stage, int wave) const {
+  __device__ __forceinline__ int64_t full() const { return K / 64; }
+  template <bool FULL>
+  __device__ __forceinline__ void issue(int64_t kt, uint32_t lds, int wave, int j0 = 0, int j1 = NI) const {
     const int64_t k0 = kt * 64;
-    if (k0 + 64 <= K) {
+    if (FULL || k0 + 64 <= K) {
       const char* b = uniform_ptr(sbase + k0 * ld);
 #pragma unroll
-      for (int j = 0; j < NI; ++j) dma16_sv(b, voff[j], stage + (wave + NW * j) * 1024);
+      for (int j = j0; j < j1; ++j) dma16_at(b, voff[j], lds + (wave + NW * j) * 1024);
     } else {
-      const char* b = sbase + k0 * ld;
 #pragma unroll
-      for (int j = 0; j < NI; ++j) {
+      for (int j = j0; j < j1; ++j) {
         const int kr = ((wave + NW * j) * 1024 + 16 * (int)(threadIdx.x & 63)) / PITCH;
-        const char* p = k0 + kr < K ? b + voff[j] : reinterpret_cast<const char*>(&g_zero_16);
-        dma16(p, stage + (wave + NW * j) * 1024);
+        const char* p = k0 + kr < K ? sbase + k0 * ld + voff[j] : reinterpret_cast<const char*>(&g_zero_16);
+        DenseK<32 * NW, 1, NW>::dma16_any(p, lds + (wave + NW * j) * 1024);
       }
     }
   }
@@ -129,19 +144,60 @@ struct DenseMN {
   }
 };
 
-// acc += the products of K-tiles kt0 .. kt1-1 (kt1 > kt0). smem: two stages. The MFMA operands
-// are swapped (transposed blocks): a lane then holds 16 columns of one row.
+// One K-tile from stage st (LDS offset lst), whose first fragments are in a[0], b[0]. A 16-k step
+// is NM MFMAs; behind each of its first ones goes a fragment read of the next step. At the last
+// step the wave holds every fragment that it needs of the stage: it waits for its own loads of
+// K-tile kt+1 and for the workgroup, then reads that tile's first fragments (from nx) and loads
+// kt+2's A into the stage that has become free, between the step's MFMAs; B follows in the first
+// step of the next K-tile, so the memory system sees two smaller bursts. sched_barrier keeps each
+// where it is put: left to itself the compiler gathers reads before the MFMAs (16384 x 4096 x 7168,
+// NT: 860 us, 810 placed; a wave's MFMA takes 32 cycles, room for its neighbour's few scalar and
+// address instructions). FULL: kt + 2 lies below both operands' full(), so no condition stays in
+// the loop (with conditions around the loads: 990 us).
+template <class Tl, bool FULL, class OA, class OB>
+__device__ __forceinline__ void dense_tile(const OA& oa, const OB& ob, int64_t kt, int64_t kt1, char* st, char* nx,
+                                           uint32_t lst, uint32_t lnx, int wave, uint4 (&a)[2][Tl::FM],
+                                           uint4 (&b)[2][Tl::FN], f32x16_t (&acc)[Tl::FM][Tl::FN]) {
+  constexpr int NM = Tl::FM * Tl::FN, NR = Tl::FM + Tl::FN, RS = (NR + NM - 1) / NM;
+  static_assert(NM >= 4 && OA::NI % (NM / 2 < OA::NI ? NM / 2 : OA::NI) == 0, "slots");
+  const bool more1 = FULL || kt + 1 < kt1, more2 = FULL || kt + 2 < kt1;
+  static_for<0, 4>([&](auto kc) {
+    constexpr int ks = decltype(kc)::value, c = ks & 1;
+    if constexpr (ks == 3) asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+    const char* fr = ks == 3 ? nx : st;
+    static_for<0, NM>([&](auto ic) {
+      constexpr int i = decltype(ic)::value;
+      Mma<bf16>::run(acc[i / Tl::FN][i % Tl::FN], b[c][i % Tl::FN], a[c][i / Tl::FN]);
+      if (ks < 3 || more1) {
+        static_for<RS * i, (RS * (i + 1) < NR ? RS * (i + 1) : NR)>([&](auto rc) {
+          constexpr int r = decltype(rc)::value;
+          if constexpr (r < Tl::FN) b[c ^ 1][r] = ob.frag(fr + OA::BYTES, r, (ks + 1) & 3);
+          else a[c ^ 1][r - Tl::FN] = oa.frag(fr, r - Tl::FN, (ks + 1) & 3);
+        });
+      }
+      constexpr int sa = i - NM / 2, sb = i - NM / 4;  // the half of the slots that A's and B's loads take
+      if constexpr (ks == 3 && sa >= 0)
+        if (more2) oa.template issue<FULL>(kt + 2, lst, wave, sa * 2 * OA::NI / NM, (sa + 1) * 2 * OA::NI / NM);
+      if constexpr (ks == 0 && sb >= 0 && sb < NM / 2)
+        if (more1)
+          ob.template issue<FULL>(kt + 1, lnx + OA::BYTES, wave, sb * 2 * OB::NI / NM, (sb + 1) * 2 * OB::NI / NM);
+      __builtin_amdgcn_sched_barrier(0);
+    });
+  });
+}
+
+// acc += the products of K-tiles kt0 .. kt1-1 (kt1 > kt0). smem: two stages. The MFMA operands are
+// swapped (transposed blocks): a lane then holds 16 columns of one row.
 template <class Tl, class OA, class OB>
 __device__ __forceinline__ void dense_loop(const OA& oa, const OB& ob, int64_t kt0, int64_t kt1, char* smem, int wave,
                                            f32x16_t (&acc)[Tl::FM][Tl::FN]) {
   constexpr int SB = OA::BYTES + OB::BYTES;
-  zero_acc<Tl>(acc);
-  oa.issue(kt0, smem, wave);
-  ob.issue(kt0, smem + OA::BYTES, wave);
+  const uint32_t lds = lds_offset(smem);
+  oa.template issue<false>(kt0, lds, wave);
+  ob.template issue<false>(kt0, lds + OA::BYTES, wave);
   if (kt0 + 1 < kt1) {
-    oa.issue(kt0 + 1, smem + SB, wave);
-    ob.issue(kt0 + 1, smem + SB + OA::BYTES, wave);
-    wait_vmcnt<OA::NI + OB::NI>();
+    oa.template issue<false>(kt0 + 1, lds + SB, wave);
+    wait_vmcnt<OA::NI>();
   } else {
     wait_vmcnt<0>();
   }
@@ -152,77 +208,66 @@ __device__ __forceinline__ void dense_loop(const OA& oa, const OB& ob, int64_t k
 #pragma unroll
   for (int fn = 0; fn < Tl::FN; ++fn) b[0][fn] = ob.frag(smem + OA::BYTES, fn, 0);
   int cur = 0;
-  for (int64_t kt = kt0; kt < kt1; ++kt) {
-    char* st = smem + cur * SB;
-    char* nx = smem + (cur ^ 1) * SB;
-    static_for<0, 4>([&](auto kc) {
-      constexpr int ks = decltype(kc)::value, c = ks & 1;
-      if constexpr (ks < 3) {
-#pragma unroll
-        for (int fm = 0; fm < Tl::FM; ++fm) a[c ^ 1][fm] = oa.frag(st, fm, ks + 1);
-#pragma unroll
-        for (int fn = 0; fn < Tl::FN; ++fn) b[c ^ 1][fn] = ob.frag(st + OA::BYTES, fn, ks + 1);
-      } else if (kt + 1 < kt1) {
-        // every fragment of this stage is in registers and this wave's loads of the next stage
-        // have landed: after the barrier both hold for the whole workgroup
-        asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
-        if (kt + 2 < kt1) {
-          oa.issue(kt + 2, st, wave);
-          ob.issue(kt + 2, st + OA::BYTES, wave);
-        }
-#pragma unroll
-        for (int fm = 0; fm < Tl::FM; ++fm) a[c ^ 1][fm] = oa.frag(nx, fm, 0);
-#pragma unroll
-        for (int fn = 0; fn < Tl::FN; ++fn) b[c ^ 1][fn] = ob.frag(nx + OA::BYTES, fn, 0);
-      }
-#pragma unroll
-      for (int fm = 0; fm < Tl::FM; ++fm)
-#pragma unroll
-        for (int fn = 0; fn < Tl::FN; ++fn) Mma<bf16>::run(acc[fm][fn], b[c][fn], a[c][fm]);
-    });
-    cur ^= 1;
-  }
+  int64_t kt = kt0;
+  for (const int64_t full = min(kt1, oa.full()); kt + 2 < full; ++kt, cur ^= 1)
+    dense_tile<Tl, true>(oa, ob, kt, kt1, smem + cur * SB, smem + (cur ^ 1) * SB, lds + cur * SB,
+                         lds + (cur ^ 1) * SB, wave, a, b, acc);
+#pragma unroll 1
+  for (; kt < kt1; ++kt, cur ^= 1)
+    dense_tile<Tl, false>(oa, ob, kt, kt1, smem + cur * SB, smem + (cur ^ 1) * SB, lds + cur * SB,
+                          lds + (cur ^ 1) * SB, wave, a, b, acc);
   __syncthreads();
 }
 
 // Hands the transposed blocks of dense_loop back through a per-wave LDS patch, every lane owning
-// eight consecutive columns of a row: f(row, col, g, u), row and col in the workgroup's tile; with
-// SW, u are the same columns of the up block 32 to the right. The patch's row pitch keeps the
+// eight consecutive columns of a row: store(pair, row, col, g, u, add), pair the index of its 64
+// columns in the wave's tile, row and col in the workgroup's; with SW, u are the same columns of the up block 32 to the right. add is what load(row, col)
+// gave, called kAhead block pairs earlier: alone on its SIMD a wave would wait out each load's
+// latency (8192 x 7168 x 4096 with an addend: 467 us, 422 ahead). The patch's row pitch keeps the
 // 16-byte writes of the 32 rows on distinct banks; a wave's LDS operations run in order.
 constexpr int kDensePatch = 68;  // floats
 
-template <class Tl, bool SW, class F>
+template <class Tl, bool SW, class L, class F>
 __device__ __forceinline__ void dense_epilogue(f32x16_t (&acc)[Tl::FM][Tl::FN], char* smem, int wave, int wm, int wn,
-                                               int lane, F&& f) {
+                                               int lane, L&& load, F&& store) {
   static_assert(Tl::FN % 2 == 0, "blocks are handed back in horizontal pairs");
+  constexpr int NP = Tl::FM * Tl::FN / 2, kAhead = NP < 3 ? NP : 3;  // block pairs
+  constexpr int LPR = SW ? 4 : 8, NI = LPR / 2;                      // lanes of a row, passes of a pair
   float* patch = reinterpret_cast<float*>(smem) + wave * (32 * kDensePatch);
   const int m = lane & 31, h = lane >> 5;
-  constexpr int LPR = SW ? 4 : 8;  // lanes of a row
-  const int r0 = lane / LPR, c0 = (lane % LPR) * 8;
+  const int r0 = wm * Tl::WTM + lane / LPR, c0 = (lane % LPR) * 8;
+  decltype(load(0, 0)) raw[kAhead][NI];
+  const auto fetch = [&](auto pc) {
+    constexpr int p = decltype(pc)::value, fm = 2 * p / Tl::FN, fn = 2 * p % Tl::FN;
 #pragma unroll
-  for (int fm = 0; fm < Tl::FM; ++fm)
+    for (int i = 0; i < NI; ++i)
+      raw[p % kAhead][i] = load(r0 + fm * 32 + (64 / LPR) * i, wn * Tl::WTN + fn * 32 + c0);
+  };
+  static_for<0, kAhead>([&](auto pc) { fetch(pc); });
+  static_for<0, NP>([&](auto pc) {
+    constexpr int p = decltype(pc)::value, fm = 2 * p / Tl::FN, fn = 2 * p % Tl::FN;
 #pragma unroll
-    for (int fn = 0; fn < Tl::FN; fn += 2) {
+    for (int b = 0; b < 2; ++b)
 #pragma unroll
-      for (int b = 0; b < 2; ++b)
+      for (int g = 0; g < 4; ++g)
+        *reinterpret_cast<float4*>(patch + m * kDensePatch + 32 * b + 8 * g + 4 * h) =
+            make_float4(acc[fm][fn + b][4 * g], acc[fm][fn + b][4 * g + 1], acc[fm][fn + b][4 * g + 2],
+                        acc[fm][fn + b][4 * g + 3]);
 #pragma unroll
-        for (int g = 0; g < 4; ++g)
-          *reinterpret_cast<float4*>(patch + m * kDensePatch + 32 * b + 8 * g + 4 * h) =
-              make_float4(acc[fm][fn + b][4 * g], acc[fm][fn + b][4 * g + 1], acc[fm][fn + b][4 * g + 2],
-                          acc[fm][fn + b][4 * g + 3]);
+    for (int i = 0; i < NI; ++i) {
+      const float* q = patch + (lane / LPR + (64 / LPR) * i) * kDensePatch + c0;
+      float g8[8], u8[8];
 #pragma unroll
-      for (int i = 0; i < LPR / 2; ++i) {
-        const int row = r0 + (64 / LPR) * i;
-        const float* p = patch + row * kDensePatch + c0;
-        float g8[8], u8[8];
-#pragma unroll
-        for (int q = 0; q < 8; ++q) {
-          g8[q] = p[q];
-          u8[q] = SW ? p[32 + q] : 0.0f;
-        }
-        f(wm * Tl::WTM + fm * 32 + row, wn * Tl::WTN + fn * 32 + c0, g8, u8);
+      for (int k = 0; k < 2; ++k) {
+        const float4 v = *reinterpret_cast<const float4*>(q + 4 * k);
+        const float4 u = SW ? *reinterpret_cast<const float4*>(q + 32 + 4 * k) : v;
+        g8[4 * k] = v.x; g8[4 * k + 1] = v.y; g8[4 * k + 2] = v.z; g8[4 * k + 3] = v.w;
+        u8[4 * k] = u.x; u8[4 * k + 1] = u.y; u8[4 * k + 2] = u.z; u8[4 * k + 3] = u.w;
       }
+      store(std::integral_constant<int, fn / 2>(), r0 + fm * 32 + (64 / LPR) * i, wn * Tl::WTN + fn * 32 + c0, g8, u8, raw[p % kAhead][i]);
     }
+    if constexpr (p + kAhead < NP) fetch(std::integral_constant<int, p + kAhead>());
+  });
 }
 
 }  // namespace mok
