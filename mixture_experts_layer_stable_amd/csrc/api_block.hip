@@ -276,7 +276,6 @@ mok_status mok_linear_forward(const mok_linear_desc* d, const void* x, const voi
   a.out = y;
   a.pre = pre;
   a.part = (float*)ws;
-  a.split = linear_split(LIN_FWD, d->act, d->epi, d->M, d->N, d->K);
   MOK_LAUNCH("linear", (hipStream_t)stream,
              launch_linear(a, LIN_FWD, d->act, d->epi, d->act == MOK_F32, (hipStream_t)stream));
   return MOK_OK;
@@ -320,7 +319,6 @@ mok_status mok_linear_backward(const mok_linear_desc* d, const void* dy, const v
     a.K = P;
     a.add = dx_add;
     a.out = dx;
-    a.split = linear_split(LIN_DX, d->act, MOK_EPI_NONE, a.M, a.N, a.K);
     MOK_LAUNCH("linear", s, launch_linear(a, LIN_DX, d->act, MOK_EPI_NONE, d->act == MOK_F32, s));
   }
   if (dw != nullptr) {
@@ -329,7 +327,6 @@ mok_status mok_linear_backward(const mok_linear_desc* d, const void* dy, const v
     a.K = d->M;
     a.add = dw_add;
     a.out = dw;
-    a.split = linear_split(LIN_DW, d->act, MOK_EPI_NONE, a.M, a.N, a.K);
     MOK_LAUNCH("linear", s, launch_linear(a, LIN_DW, d->act, MOK_EPI_NONE,
                                           d->act == MOK_F32 || (d->flags & MOK_FLAG_WGRAD_F32) != 0, s));
   }

@@ -84,13 +84,17 @@ struct LinearArgs {
   void* out;          // [M][N]
   void* pre;          // LIN_FWD: [M][P], or nullptr
   float* part;        // partial products of a split K: [split][M][P] fp32
+  int split;          // set by launch_linear
+};
+// Tile and slices of K of a product: a function of the shape and type only, so that the sums are.
+struct LinearPlan {
+  int tile;   // 0..3: 256x256, 128x128, 64x128, 32x128 (bf16); 0 for fp32
   int split;
 };
-// Slices of K (workspace: linear_part_bytes); a function of the shape and type only.
-int linear_split(int kind, int act, int epi, int64_t M, int N, int64_t K);
+LinearPlan linear_plan(int kind, int act, int epi, int64_t M, int N, int64_t K);
 size_t linear_part_bytes(int kind, int act, int epi, int64_t M, int N, int64_t K);
 hipError_t launch_linear(const LinearArgs& a, int kind, int act, int epi, bool out_f32, hipStream_t s);
-hipError_t launch_linear_bf16(const LinearArgs& a, int kind, int epi, bool out_f32, hipStream_t s);  // linear_dense.hip
+hipError_t launch_linear_bf16(const LinearArgs& a, int tile, int kind, int epi, bool out_f32, hipStream_t s);
 
 // dp = dy f'(pre) (epi != NONE; dp may be nullptr with NONE) and the column sums' parts
 // [linear_db_parts][P] fp32 (nullptr: not formed)

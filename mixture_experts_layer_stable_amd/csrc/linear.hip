@@ -209,15 +209,51 @@ void run_dpre(const void* dy, const void* pre, int64_t M, int N, int epi, void* 
 
 }  // namespace
 
-int linear_split(int, int, int, int64_t, int, int64_t) { return 1; }
+// The plan of least estimated time. A tile's time is its K-tiles times what one takes (half as long
+// on an empty chip as on a full one), plus a fixed part (first loads, epilogue); the tiles go out in
+// rounds of as many as fit the 256 CUs. Slices of K cost their fp32 partial products' way to memory
+// and back, and a second launch that reads them one after the other. The constants (us) are fitted
+// to 28 shapes from 1 to 16384 rows at every tile and split: the plan taken is the fastest or within
+// a tenth of it.
+LinearPlan linear_plan(int kind, int act, int epi, int64_t M, int N, int64_t K) {
+  LinearPlan best{0, 1};
+  if (act == MOK_F32 || M == 0) return best;
+  struct Tile {
+    int bm, bn, per_cu;
+    double ktile, fixed;
+  };
+  static const Tile kTiles[4] = {
+      {256, 256, 1, 1.55, 11.0}, {128, 128, 2, 1.1, 5.0}, {64, 128, 3, 1.1, 4.0}, {32, 128, 4, 1.2, 3.5}};
+  const int64_t P = epi == MOK_EPI_SWIGLU ? 2 * (int64_t)N : N, kt = (K + 63) / 64;
+  double least = 1e30;
+  for (int t = 0; t < 4; ++t) {
+    const Tile& c = kTiles[t];
+    const int64_t tiles = ((M + c.bm - 1) / c.bm) * ((P + c.bn - 1) / c.bn), slots = 256 * c.per_cu;
+    for (int split = 1; split <= 32; split *= 2) {
+      if (split > 1 && kt / split < 2) break;
+      const double rounds = (double)((tiles * split + slots - 1) / slots);
+      const double fill = std::min(1.0, (double)(tiles * split) / (double)slots);
+      double us = rounds * ((double)((kt + split - 1) / split) * c.ktile * (0.5 + 0.5 * fill) + c.fixed);
+      if (split > 1) us += 4.0 + 0.25 * split + 8.0 * split * (double)M * (double)P / 4e6;
+      if (us < least) {
+        least = us;
+        best = {t, split};
+      }
+    }
+  }
+  return best;
+}
 
 size_t linear_part_bytes(int kind, int act, int epi, int64_t M, int N, int64_t K) {
-  const int split = linear_split(kind, act, epi, M, N, K);
+  const int split = linear_plan(kind, act, epi, M, N, K).split;
   return split > 1 ? 4 * (size_t)split * (size_t)M * (epi == MOK_EPI_SWIGLU ? 2 * N : N) : 0;
 }
 
-hipError_t launch_linear(const LinearArgs& a, int kind, int act, int epi, bool out_f32, hipStream_t s) {
-  if (act == MOK_BF16) return launch_linear_bf16(a, kind, epi, out_f32, s);
+hipError_t launch_linear(const LinearArgs& args, int kind, int act, int epi, bool out_f32, hipStream_t s) {
+  LinearArgs a = args;
+  const LinearPlan p = linear_plan(kind, act, epi, a.M, a.N, a.K);
+  a.split = p.split;
+  if (act == MOK_BF16) return launch_linear_bf16(a, p.tile, kind, epi, out_f32, s);
   run_kind<float>(a, kind, epi, out_f32, s);
   return hipGetLastError();
 }

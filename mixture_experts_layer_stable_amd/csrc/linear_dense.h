@@ -1,6 +1,6 @@
 // bf16 matrix product on direct global->LDS loads, for the products of linear.hip.
 //
-// A workgroup of four waves multiplies one BM x BN tile, a wave a quarter of it; both operands
+// A workgroup multiplies one BM x BN tile, each wave its part of it; both operands
 // of a 64-element K-tile arrive in one of two LDS stages by global_load_lds_dwordx4 (gemm2.h's
 // tile layouts, with ragged edges). With 256 x 256 tiles a SIMD holds one wave (256 fp32
 // accumulators per lane), so nothing but the order of its own instructions hides its loads: every
@@ -96,6 +96,9 @@ struct DenseMN {
   static constexpr int BYTES = 64 * PITCH;
   static constexpr int NI = BYTES / (1024 * NW);
   static_assert(BYTES % (1024 * NW) == 0 && PITCH <= 1024, "tile");
+  // chunk c of k-row k lies at chunk c ^ swz(k): the four rows that a transposing read covers are
+  // on distinct banks (rows of 64 bytes are by themselves, of 128 bytes every other one)
+  static __device__ __forceinline__ int swz(int k) { return ROWS >= 128 ? 4 * (k & 3) : (ROWS == 64 ? 2 * (k & 2) : 0); }
   const char* sbase;
   int64_t ld, K;
   uint32_t voff[NI];
@@ -110,7 +113,7 @@ struct DenseMN {
 #pragma unroll
     for (int j = 0; j < NI; ++j) {
       const int o = (wave + NW * j) * 1024 + 16 * lane, kr = o / PITCH;
-      const int ch = ((o % PITCH) >> 4) ^ swz_mn(kr);
+      const int ch = ((o % PITCH) >> 4) ^ swz(kr);
       voff[j] = (uint32_t)(kr * ld_bytes) + (8 * ch < cols ? 16u * (uint32_t)ch : 0u);
     }
     const int g = lane >> 4, i = lane & 15;
@@ -118,7 +121,7 @@ struct DenseMN {
 #pragma unroll
     for (int f = 0; f < NF; ++f) {
       const int mn = fcol(f) + 16 * (g & 1) + 4 * (i & 3);
-      foff[f] = k0 * PITCH + 16 * ((mn >> 3) ^ swz_mn(k0)) + 2 * (mn & 7);
+      foff[f] = k0 * PITCH + 16 * ((mn >> 3) ^ swz(k0)) + 2 * (mn & 7);
     }
   }
   __device__ __forceinline__ int64_t full() const { return K / 64; }
@@ -159,7 +162,7 @@ __device__ __forceinline__ void dense_tile(const OA& oa, const OB& ob, int64_t k
                                            uint32_t lst, uint32_t lnx, int wave, uint4 (&a)[2][Tl::FM],
                                            uint4 (&b)[2][Tl::FN], f32x16_t (&acc)[Tl::FM][Tl::FN]) {
   constexpr int NM = Tl::FM * Tl::FN, NR = Tl::FM + Tl::FN, RS = (NR + NM - 1) / NM;
-  static_assert(NM >= 4 && OA::NI % (NM / 2 < OA::NI ? NM / 2 : OA::NI) == 0, "slots");
+  constexpr int HALF = NM > 1 ? NM / 2 : 1;  // MFMA slots that an operand's loads are spread over
   const bool more1 = FULL || kt + 1 < kt1, more2 = FULL || kt + 2 < kt1;
   static_for<0, 4>([&](auto kc) {
     constexpr int ks = decltype(kc)::value, c = ks & 1;
@@ -175,12 +178,12 @@ __device__ __forceinline__ void dense_tile(const OA& oa, const OB& ob, int64_t k
           else a[c ^ 1][r - Tl::FN] = oa.frag(fr, r - Tl::FN, (ks + 1) & 3);
         });
       }
-      constexpr int sa = i - NM / 2, sb = i - NM / 4;  // the half of the slots that A's and B's loads take
+      constexpr int sa = i - (NM - HALF), sb = i - NM / 4;
       if constexpr (ks == 3 && sa >= 0)
-        if (more2) oa.template issue<FULL>(kt + 2, lst, wave, sa * 2 * OA::NI / NM, (sa + 1) * 2 * OA::NI / NM);
-      if constexpr (ks == 0 && sb >= 0 && sb < NM / 2)
+        if (more2) oa.template issue<FULL>(kt + 2, lst, wave, sa * OA::NI / HALF, (sa + 1) * OA::NI / HALF);
+      if constexpr (ks == 0 && sb >= 0 && sb < HALF)
         if (more1)
-          ob.template issue<FULL>(kt + 1, lnx + OA::BYTES, wave, sb * 2 * OB::NI / NM, (sb + 1) * 2 * OB::NI / NM);
+          ob.template issue<FULL>(kt + 1, lnx + OA::BYTES, wave, sb * OB::NI / HALF, (sb + 1) * OB::NI / HALF);
       __builtin_amdgcn_sched_barrier(0);
     });
   });

@@ -7,8 +7,9 @@ namespace {
 
 constexpr int kBand = 8;  // tile rows of a band of the tile walk
 
-template <class Tl, int KIND, int EPI, typename TO>
-__global__ __launch_bounds__(Tl::NT, 1) void linear_dense_kernel(LinearArgs a) {
+// PART: the tile's sums over this slice of K go to a.part; linear_join_kernel adds the slices.
+template <class Tl, int KIND, int EPI, typename TO, bool PART>
+__global__ __launch_bounds__(Tl::NT) void linear_dense_kernel(LinearArgs a) {
   constexpr bool SW = EPI == MOK_EPI_SWIGLU;
   // 256 x 256 tiles belong to outputs that no cache keeps: stored past L2, they leave it to the
   // operands' bands (16384 x (2 x 2048) x 7168: 818 -> 745 us)
@@ -56,6 +57,19 @@ __global__ __launch_bounds__(Tl::NT, 1) void linear_dense_kernel(LinearArgs a) {
   zero_acc<Tl>(acc);
   if (kt1 > kt0) dense_loop<Tl>(oa, ob, kt0, kt1, smem, wave, acc);
 
+  const auto in = [&](int row, int j) { return m0 + row < a.M && col(j) < a.N; };
+  if constexpr (PART) {
+    float* part = a.part + (int64_t)slice * a.M * (SW ? 2 * a.N : a.N);
+    dense_epilogue<Tl, SW>(
+        acc, smem, wave, wm, wn, lane, [](int, int) { return 0; },
+        [&](auto, int row, int j, float (&g)[8], float (&u)[8], int) {
+          if (!in(row, j)) return;
+          float* p = part + (m0 + row) * (SW ? 2 * a.N : a.N) + col(j);
+          store8(p, g);
+          if constexpr (SW) store8(p + a.N, u);
+        });
+    return;
+  }
   // bias of the eight columns that this lane stores of each block pair
   constexpr int LPR = SW ? 4 : 8;
   float bg[Tl::FN / 2][8], bu[Tl::FN / 2][8];
@@ -66,7 +80,6 @@ __global__ __launch_bounds__(Tl::NT, 1) void linear_dense_kernel(LinearArgs a) {
     const int c = col(wn * Tl::WTN + 64 * p + (lane % LPR) * 8);
     if (KIND == LIN_FWD && c < a.N) linear_bias8<EPI>(a, c, bg[p], bu[p]);
   }
-  const auto in = [&](int row, int j) { return m0 + row < a.M && col(j) < a.N; };
   dense_epilogue<Tl, SW>(
       acc, smem, wave, wm, wn, lane,
       [&](int row, int j) { return in(row, j) ? linear_add8<TO>(a, m0 + row, col(j)) : Raw8<TO>{}; },
@@ -83,11 +96,49 @@ __global__ __launch_bounds__(Tl::NT, 1) void linear_dense_kernel(LinearArgs a) {
       });
 }
 
+// out = f(sum of the slices' partial products + bias) + add: eight columns of a row per thread.
+template <int KIND, int EPI, typename TO>
+__global__ __launch_bounds__(256) void linear_join_kernel(LinearArgs a) {
+  constexpr bool SW = EPI == MOK_EPI_SWIGLU;
+  const int64_t nv = a.N / 8, i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (i >= a.M * nv) return;
+  const int64_t m = i / nv, P = SW ? 2 * a.N : a.N;
+  const int c = (int)(i - m * nv) * 8;
+  const Raw8<TO> add = linear_add8<TO>(a, m, c);
+  float g[8], u[8];
+#pragma unroll
+  for (int q = 0; q < 8; ++q) g[q] = u[q] = 0.0f;
+#pragma unroll 4
+  for (int s = 0; s < a.split; ++s) {
+    const float* p = a.part + ((int64_t)s * a.M + m) * P + c;
+    float v[8];
+    load8(p, v);
+#pragma unroll
+    for (int q = 0; q < 8; ++q) g[q] += v[q];
+    if constexpr (SW) {
+      load8(p + a.N, v);
+#pragma unroll
+      for (int q = 0; q < 8; ++q) u[q] += v[q];
+    }
+  }
+  if constexpr (KIND == LIN_FWD) linear_bias8<EPI>(a, c, g, u);
+  linear_store8<KIND, EPI, TO, bf16>(a, m, c, g, u, add);
+}
+
 template <class Tl, int KIND, int EPI, typename TO>
 void run(const LinearArgs& a, hipStream_t s) {
-  const int bn = EPI == MOK_EPI_SWIGLU ? Tl::BN / 2 : Tl::BN;
+  constexpr bool SW = EPI == MOK_EPI_SWIGLU;
+  const int bn = SW ? Tl::BN / 2 : Tl::BN;
   const int64_t tiles = (int64_t)((a.N + bn - 1) / bn) * ((a.M + Tl::BM - 1) / Tl::BM);
-  hipLaunchKernelGGL((linear_dense_kernel<Tl, KIND, EPI, TO>), dim3((unsigned)(tiles * a.split)), dim3(Tl::NT), 0, s, a);
+  const dim3 grid((unsigned)(tiles * a.split)), block(Tl::NT);
+  if (a.split == 1) {
+    hipLaunchKernelGGL((linear_dense_kernel<Tl, KIND, EPI, TO, false>), grid, block, 0, s, a);
+    return;
+  }
+  hipLaunchKernelGGL((linear_dense_kernel<Tl, KIND, SW ? MOK_EPI_SWIGLU : MOK_EPI_NONE, bf16, true>), grid, block, 0, s,
+                     a);
+  hipLaunchKernelGGL((linear_join_kernel<KIND, EPI, TO>), dim3((unsigned)((a.M * (a.N / 8) + 255) / 256)), dim3(256), 0,
+                     s, a);
 }
 
 template <class Tl>
@@ -108,8 +159,11 @@ void run_tile(const LinearArgs& a, int kind, int epi, bool out_f32, hipStream_t 
 
 }  // namespace
 
-hipError_t launch_linear_bf16(const LinearArgs& a, int kind, int epi, bool out_f32, hipStream_t s) {
-  run_tile<Tiling<256, 256, 2, 2>>(a, kind, epi, out_f32, s);
+hipError_t launch_linear_bf16(const LinearArgs& a, int tile, int kind, int epi, bool out_f32, hipStream_t s) {
+  if (tile == 0) run_tile<Tiling<256, 256, 2, 2>>(a, kind, epi, out_f32, s);
+  else if (tile == 1) run_tile<Tiling<128, 128, 2, 2>>(a, kind, epi, out_f32, s);
+  else if (tile == 2) run_tile<Tiling<64, 128, 1, 2>>(a, kind, epi, out_f32, s);
+  else run_tile<Tiling<32, 128, 1, 2>>(a, kind, epi, out_f32, s);
   return hipGetLastError();
 }
 
