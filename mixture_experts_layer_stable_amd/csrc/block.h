@@ -88,7 +88,7 @@ struct LinearArgs {
 };
 // Tile and slices of K of a product: a function of the shape and type only, so that the sums are.
 struct LinearPlan {
-  int tile;   // 0..3: 256x256, 128x128, 64x128, 32x128 (bf16); 0 for fp32
+  int tile;   // 0..3: 256x256, 128x128, 64x128, 32x128 (bf16); 0, 1: 128x128, 64x64 (SWIGLU 64x128) (fp32)
   int split;
 };
 LinearPlan linear_plan(int kind, int act, int epi, int64_t M, int N, int64_t K);

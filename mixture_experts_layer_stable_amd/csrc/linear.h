@@ -111,4 +111,34 @@ __device__ __forceinline__ void linear_bias8(const LinearArgs& a, int c, float (
   }
 }
 
+// out = f(sum of the slices' partial products + bias) + add: eight columns of a row per thread.
+// T: type of the operands.
+template <int KIND, int EPI, typename TO, typename T>
+__global__ __launch_bounds__(256) void linear_join_kernel(LinearArgs a) {
+  constexpr bool SW = EPI == MOK_EPI_SWIGLU;
+  const int64_t nv = a.N / 8, i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (i >= a.M * nv) return;
+  const int64_t m = i / nv, P = SW ? 2 * a.N : a.N;
+  const int c = (int)(i - m * nv) * 8;
+  const Raw8<TO> add = linear_add8<TO>(a, m, c);
+  float g[8], u[8];
+#pragma unroll
+  for (int q = 0; q < 8; ++q) g[q] = u[q] = 0.0f;
+#pragma unroll 4
+  for (int s = 0; s < a.split; ++s) {
+    const float* p = a.part + ((int64_t)s * a.M + m) * P + c;
+    float v[8];
+    load8(p, v);
+#pragma unroll
+    for (int q = 0; q < 8; ++q) g[q] += v[q];
+    if constexpr (SW) {
+      load8(p + a.N, v);
+#pragma unroll
+      for (int q = 0; q < 8; ++q) u[q] += v[q];
+    }
+  }
+  if constexpr (KIND == LIN_FWD) linear_bias8<EPI>(a, c, g, u);
+  linear_store8<KIND, EPI, TO, T>(a, m, c, g, u, add);
+}
+
 }  // namespace mok

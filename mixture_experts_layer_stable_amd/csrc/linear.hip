@@ -48,31 +48,33 @@ struct MnSource {
   }
 };
 
-using Tile = Tiling<128, 128, 2, 2>;
-
-// One 128x128 tile per workgroup: operands staged through registers into a double-buffered
-// LDS tile (gemm.h), right for every shape and type.
-template <typename T, int KIND, int EPI, typename TO>
+// One tile per workgroup: operands staged through registers into a double-buffered LDS tile
+// (gemm.h). PART: the tile's sums over a slice of K, for linear_join_kernel.
+template <class Tile, typename T, int KIND, int EPI, typename TO, bool PART>
 __global__ __launch_bounds__(256) void linear_simple_kernel(LinearArgs a) {
-  __shared__ __align__(1024) char smem[Tile::LDS_BYTES];
+  constexpr int PATCH = Tile::NW * 32 * kPatchLd * 4;  // the epilogue's
+  __shared__ __align__(1024) char smem[Tile::LDS_BYTES > PATCH ? Tile::LDS_BYTES : PATCH];
   constexpr bool SW = EPI == MOK_EPI_SWIGLU;
   constexpr int BKE = kRowBytes / (int)sizeof(T);
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, wm = wave >> 1, wn = wave & 1;
   constexpr int BN = SW ? Tile::BN / 2 : Tile::BN;  // outputs of a tile's columns
-  const int NT = (a.N + BN - 1) / BN;
-  const int64_t m0 = (int64_t)(blockIdx.x / NT) * Tile::BM;
-  const int n0 = (blockIdx.x % NT) * BN;
-  const int KT = (int)((a.K + BKE - 1) / BKE);
+  const int NT = (a.N + BN - 1) / BN, MT = (int)((a.M + Tile::BM - 1) / Tile::BM);
+  const int slice = blockIdx.x / (MT * NT), L = blockIdx.x - slice * (MT * NT);
+  const int64_t m0 = (int64_t)(L / NT) * Tile::BM;
+  const int n0 = (L % NT) * BN;
+  const int64_t tiles = (a.K + BKE - 1) / BKE, kt0 = tiles * slice / a.split, kt1 = tiles * (slice + 1) / a.split;
+  const int64_t k0 = kt0 * BKE, k1 = min(a.K, kt1 * BKE);  // this slice
+  const int KT = (int)(kt1 - kt0);
   f32x16_t acc[Tile::FM][Tile::FN];
-  const T* A = (const T*)a.a;
-  const T* B = (const T*)a.b;
+  const T* A = (const T*)a.a + (KIND == LIN_DW ? k0 * a.M : k0);
+  const T* B = (const T*)a.b + (KIND == LIN_FWD ? k0 : k0 * a.N);
   // first output column of tile column j (SWIGLU: 32-column blocks of gate and up in turn)
   const auto col = [&](int j) { return SW ? n0 + (j / Tile::WTN) * (Tile::WTN / 2) + (j & 31) : n0 + j; };
   if constexpr (KIND == LIN_FWD) {
     KTailStager<T, Tile::BM> sa;
-    sa.init(tid, a.K, [&](int r) { return m0 + r < a.M ? A + (m0 + r) * a.K : nullptr; });
+    sa.init(tid, k1 - k0, [&](int r) { return m0 + r < a.M ? A + (m0 + r) * a.K : nullptr; });
     KTailStager<T, Tile::BN> sb;
-    sb.init(tid, a.K, [&](int j) -> const T* {
+    sb.init(tid, k1 - k0, [&](int j) -> const T* {
       const int c = col(j);
       if (c >= a.N) return nullptr;
       return B + (int64_t)(SW && (j & 32) ? a.N + c : c) * a.K;
@@ -80,18 +82,18 @@ __global__ __launch_bounds__(256) void linear_simple_kernel(LinearArgs a) {
     main_loop<T, Tile>(sa, sb, KT, smem, wm, wn, lane, acc);
   } else if constexpr (KIND == LIN_DX) {
     KTailStager<T, Tile::BM> sa;
-    sa.init(tid, a.K, [&](int r) { return m0 + r < a.M ? A + (m0 + r) * a.K : nullptr; });
+    sa.init(tid, k1 - k0, [&](int r) { return m0 + r < a.M ? A + (m0 + r) * a.K : nullptr; });
     MNStager<T, Tile::BN, MnSource<T>> sb;
     sb.tid = tid;
-    sb.src = MnSource<T>{B, a.N, a.K, a.N, n0};
+    sb.src = MnSource<T>{B, a.N, k1 - k0, a.N, n0};
     main_loop<T, Tile>(sa, sb, KT, smem, wm, wn, lane, acc);
   } else {
     MNStager<T, Tile::BM, MnSource<T>> sa;
     sa.tid = tid;
-    sa.src = MnSource<T>{A, a.M, a.K, a.M, m0};
+    sa.src = MnSource<T>{A, a.M, k1 - k0, a.M, m0};
     MNStager<T, Tile::BN, MnSource<T>> sb;
     sb.tid = tid;
-    sb.src = MnSource<T>{B, a.N, a.K, a.N, n0};
+    sb.src = MnSource<T>{B, a.N, k1 - k0, a.N, n0};
     main_loop<T, Tile>(sa, sb, KT, smem, wm, wn, lane, acc);
   }
   __syncthreads();
@@ -99,7 +101,7 @@ __global__ __launch_bounds__(256) void linear_simple_kernel(LinearArgs a) {
                        [&](int row, int j, const float (&g)[16], const float (&u)[16]) {
     const int64_t m = m0 + row;
     if (m >= a.M) return;
-    const int c = col(j);
+    const int c = col(j), P = SW ? 2 * a.N : a.N;
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       if (c + 8 * h >= a.N) continue;
@@ -109,33 +111,41 @@ __global__ __launch_bounds__(256) void linear_simple_kernel(LinearArgs a) {
         g8[i] = g[8 * h + i];
         u8[i] = SW ? u[8 * h + i] : 0.0f;
       }
+      if constexpr (PART) {
+        float* p = a.part + ((int64_t)slice * a.M + m) * P + c + 8 * h;
+        store8(p, g8);
+        if constexpr (SW) store8(p + a.N, u8);
+        continue;
+      }
       if constexpr (KIND == LIN_FWD) linear_bias8<EPI>(a, c + 8 * h, g8, u8);
       linear_store8<KIND, EPI, TO, T>(a, m, c + 8 * h, g8, u8, linear_add8<TO>(a, m, c + 8 * h));
     }
   });
 }
 
-template <typename T, int KIND, int EPI, typename TO>
+template <class Tile, int KIND, int EPI>
 void run_simple(const LinearArgs& a, hipStream_t s) {
-  const int bn = EPI == MOK_EPI_SWIGLU ? Tile::BN / 2 : Tile::BN;
-  const dim3 grid((unsigned)(((a.N + bn - 1) / bn) * ((a.M + Tile::BM - 1) / Tile::BM)));
-  hipLaunchKernelGGL((linear_simple_kernel<T, KIND, EPI, TO>), grid, dim3(256), 0, s, a);
+  constexpr bool SW = EPI == MOK_EPI_SWIGLU;
+  const int bn = SW ? Tile::BN / 2 : Tile::BN;
+  const dim3 grid((unsigned)((int64_t)((a.N + bn - 1) / bn) * ((a.M + Tile::BM - 1) / Tile::BM) * a.split));
+  if (a.split == 1) {
+    hipLaunchKernelGGL((linear_simple_kernel<Tile, float, KIND, EPI, float, false>), grid, dim3(256), 0, s, a);
+    return;
+  }
+  hipLaunchKernelGGL((linear_simple_kernel<Tile, float, KIND, SW ? MOK_EPI_SWIGLU : MOK_EPI_NONE, float, true>), grid,
+                     dim3(256), 0, s, a);
+  hipLaunchKernelGGL((linear_join_kernel<KIND, EPI, float, float>), dim3((unsigned)((a.M * (a.N / 8) + 255) / 256)),
+                     dim3(256), 0, s, a);
 }
 
-template <typename T>
-void run_kind(const LinearArgs& a, int kind, int epi, bool out_f32, hipStream_t s) {
-  if (kind == LIN_FWD) {
-    if (epi == MOK_EPI_NONE) run_simple<T, LIN_FWD, MOK_EPI_NONE, T>(a, s);
-    else if (epi == MOK_EPI_SILU) run_simple<T, LIN_FWD, MOK_EPI_SILU, T>(a, s);
-    else if (epi == MOK_EPI_GELU) run_simple<T, LIN_FWD, MOK_EPI_GELU, T>(a, s);
-    else run_simple<T, LIN_FWD, MOK_EPI_SWIGLU, T>(a, s);
-  } else if (kind == LIN_DX) {
-    run_simple<T, LIN_DX, MOK_EPI_NONE, T>(a, s);
-  } else if (out_f32) {
-    run_simple<T, LIN_DW, MOK_EPI_NONE, float>(a, s);
-  } else {
-    run_simple<T, LIN_DW, MOK_EPI_NONE, T>(a, s);
-  }
+template <class Tile>
+void run_f32(const LinearArgs& a, int kind, int epi, hipStream_t s) {
+  if (kind == LIN_DX) run_simple<Tile, LIN_DX, MOK_EPI_NONE>(a, s);
+  else if (kind == LIN_DW) run_simple<Tile, LIN_DW, MOK_EPI_NONE>(a, s);
+  else if (epi == MOK_EPI_NONE) run_simple<Tile, LIN_FWD, MOK_EPI_NONE>(a, s);
+  else if (epi == MOK_EPI_SILU) run_simple<Tile, LIN_FWD, MOK_EPI_SILU>(a, s);
+  else if (epi == MOK_EPI_GELU) run_simple<Tile, LIN_FWD, MOK_EPI_GELU>(a, s);
+  else if constexpr (Tile::FN % 2 == 0) run_simple<Tile, LIN_FWD, MOK_EPI_SWIGLU>(a, s);  // gate and up side by side
 }
 
 // ---- dp = dy f'(pre), and the parts of the bias gradient ----
@@ -217,17 +227,20 @@ void run_dpre(const void* dy, const void* pre, int64_t M, int N, int epi, void* 
 // a tenth of it.
 LinearPlan linear_plan(int kind, int act, int epi, int64_t M, int N, int64_t K) {
   LinearPlan best{0, 1};
-  if (act == MOK_F32 || M == 0) return best;
+  if (M == 0) return best;
   struct Tile {
     int bm, bn, per_cu;
     double ktile, fixed;
   };
   static const Tile kTiles[4] = {
       {256, 256, 1, 1.55, 11.0}, {128, 128, 2, 1.1, 5.0}, {64, 128, 3, 1.1, 4.0}, {32, 128, 4, 1.2, 3.5}};
-  const int64_t P = epi == MOK_EPI_SWIGLU ? 2 * (int64_t)N : N, kt = (K + 63) / 64;
+  static const Tile kTilesF32[2] = {{128, 128, 2, 4.6, 6.0}, {64, 64, 4, 2.9, 5.0}};  // K-tiles of 32
+  static const Tile kTilesF32Sw[2] = {{128, 128, 2, 4.6, 6.0}, {64, 128, 3, 3.6, 5.0}};
+  const bool f32 = act == MOK_F32;
+  const int64_t P = epi == MOK_EPI_SWIGLU ? 2 * (int64_t)N : N, kt = f32 ? (K + 31) / 32 : (K + 63) / 64;
   double least = 1e30;
-  for (int t = 0; t < 4; ++t) {
-    const Tile& c = kTiles[t];
+  for (int t = 0; t < (f32 ? 2 : 4); ++t) {
+    const Tile& c = f32 ? (epi == MOK_EPI_SWIGLU ? kTilesF32Sw[t] : kTilesF32[t]) : kTiles[t];
     const int64_t tiles = ((M + c.bm - 1) / c.bm) * ((P + c.bn - 1) / c.bn), slots = 256 * c.per_cu;
     for (int split = 1; split <= 32; split *= 2) {
       if (split > 1 && kt / split < 2) break;
@@ -254,7 +267,9 @@ hipError_t launch_linear(const LinearArgs& args, int kind, int act, int epi, boo
   const LinearPlan p = linear_plan(kind, act, epi, a.M, a.N, a.K);
   a.split = p.split;
   if (act == MOK_BF16) return launch_linear_bf16(a, p.tile, kind, epi, out_f32, s);
-  run_kind<float>(a, kind, epi, out_f32, s);
+  if (p.tile == 0) run_f32<Tiling<128, 128, 2, 2>>(a, kind, epi, s);
+  else if (epi == MOK_EPI_SWIGLU) run_simple<Tiling<64, 128, 2, 2>, LIN_FWD, MOK_EPI_SWIGLU>(a, s);
+  else run_f32<Tiling<64, 64, 2, 2>>(a, kind, epi, s);
   return hipGetLastError();
 }
 

@@ -96,35 +96,6 @@ __global__ __launch_bounds__(Tl::NT) void linear_dense_kernel(LinearArgs a) {
       });
 }
 
-// out = f(sum of the slices' partial products + bias) + add: eight columns of a row per thread.
-template <int KIND, int EPI, typename TO>
-__global__ __launch_bounds__(256) void linear_join_kernel(LinearArgs a) {
-  constexpr bool SW = EPI == MOK_EPI_SWIGLU;
-  const int64_t nv = a.N / 8, i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (i >= a.M * nv) return;
-  const int64_t m = i / nv, P = SW ? 2 * a.N : a.N;
-  const int c = (int)(i - m * nv) * 8;
-  const Raw8<TO> add = linear_add8<TO>(a, m, c);
-  float g[8], u[8];
-#pragma unroll
-  for (int q = 0; q < 8; ++q) g[q] = u[q] = 0.0f;
-#pragma unroll 4
-  for (int s = 0; s < a.split; ++s) {
-    const float* p = a.part + ((int64_t)s * a.M + m) * P + c;
-    float v[8];
-    load8(p, v);
-#pragma unroll
-    for (int q = 0; q < 8; ++q) g[q] += v[q];
-    if constexpr (SW) {
-      load8(p + a.N, v);
-#pragma unroll
-      for (int q = 0; q < 8; ++q) u[q] += v[q];
-    }
-  }
-  if constexpr (KIND == LIN_FWD) linear_bias8<EPI>(a, c, g, u);
-  linear_store8<KIND, EPI, TO, bf16>(a, m, c, g, u, add);
-}
-
 template <class Tl, int KIND, int EPI, typename TO>
 void run(const LinearArgs& a, hipStream_t s) {
   constexpr bool SW = EPI == MOK_EPI_SWIGLU;
@@ -137,7 +108,7 @@ void run(const LinearArgs& a, hipStream_t s) {
   }
   hipLaunchKernelGGL((linear_dense_kernel<Tl, KIND, SW ? MOK_EPI_SWIGLU : MOK_EPI_NONE, bf16, true>), grid, block, 0, s,
                      a);
-  hipLaunchKernelGGL((linear_join_kernel<KIND, EPI, TO>), dim3((unsigned)((a.M * (a.N / 8) + 255) / 256)), dim3(256), 0,
+  hipLaunchKernelGGL((linear_join_kernel<KIND, EPI, TO, bf16>), dim3((unsigned)((a.M * (a.N / 8) + 255) / 256)), dim3(256), 0,
                      s, a);
 }
 
