@@ -213,6 +213,7 @@ mok_status mok_balance_forward(const mok_balance_desc* d, const float* logits, c
   a.wc = (int32_t*)(wb + w.c);
   a.wn = (int32_t*)(wb + w.n);
   a.wz = (float*)(wb + w.z);
+  a.done = (int32_t*)(wb + w.done);
   a.wl = (double*)(wb + w.loss);
   MOK_LAUNCH("balance", (hipStream_t)stream, launch_balance_fwd(a, (hipStream_t)stream));
   return MOK_OK;

@@ -1,13 +1,14 @@
 // Balance loss of the router: scores, per-expert counts and sums over ragged segments, and the
 // gradient by the logits.
 //
-// Forward, three launches: (1) a workgroup takes a chunk of consecutive tokens; a group of G
-// lanes holds one token's logits in registers (one read), forms its scores and adds them to
-// the lanes' own per-expert sums; slots are counted with integer LDS atomics; where a segment
-// ends inside the chunk the sums are written out as the partial row of (chunk, segment).
-// (2) one workgroup per (64 experts, segment) adds the segment's partial rows in chunk order.
-// (3) one workgroup adds the parts of the loss. No float atomics: the sums depend on T, E and
-// the segments only. Bound by HBM (logits read once) or, for small batches, by the launches.
+// Forward, two launches: (1) a workgroup takes a chunk of consecutive tokens; a group of G lanes
+// holds one token's logits in registers (one read, the next token's on their way), forms its
+// scores and adds them to the lanes' own per-expert sums; slots are counted with integer LDS
+// atomics; where a segment ends inside the chunk the sums are written out as the partial row of
+// (chunk, segment). (2) one workgroup per (64 experts, segment) adds the segment's partial rows;
+// the last of them adds the parts of the loss. Batches of up to 2^14 logits take one launch of one
+// workgroup for all of it. No float atomics: the sums depend on T, E and the segments only. Bound
+// by HBM (logits read once) or, for small batches, by the launches.
 // Backward: one launch, one read of the logits and one write of their gradient.
 #include <cmath>
 
@@ -19,7 +20,10 @@ namespace mok {
 namespace {
 
 constexpr int kThreadsB = 256;
-constexpr int kBalanceChunks = 512;  // two workgroups per CU
+// Four workgroups per CU, as long as a chunk keeps 32 rows.
+constexpr int kBalanceChunks = 1024, kBalanceRows = 32;
+constexpr int64_t kBalanceSmall = 1 << 14;  // logits of a batch for one workgroup
+constexpr int kBalanceSmallSegs = 64;
 
 // Logits of one token over G lanes: J vectors of VEC per lane (vector j*G + lane), at most 16
 // values. VEC = 4 where the rows are 16-byte aligned (E a multiple of 4).
@@ -66,13 +70,42 @@ __device__ __forceinline__ float lanes_max(float v, int G) {
   return v;
 }
 
-// sig(z) * exp(-top) with top = min(largest z of the token, 0): the normalised sigmoid scores
-// do not change by the factor, and a token whose every logit is far below 0 keeps its digits.
-// *slope (when asked for) receives 1 - sig(z), without a cancellation.
-__device__ __forceinline__ float scaled_sigmoid(float z, float top, float* slope = nullptr) {
-  const float e = expf(-fabsf(z)), d = 1.0f / (1.0f + e);
-  if (slope != nullptr) *slope = z > 0.0f ? e * d : d;
-  return expf(fminf(z, 0.0f) - top) * d;
+// exp(x) for x <= 0 to two steps of fp32: the hardware's exp2 of the rounded product, corrected
+// by the product's own rounding error. Below -150 it is 0 (a NaN stays one); the library's expf,
+// for every range, made these kernels vector-ALU bound (131072 x 256 sigmoid forward 96 us).
+__device__ __forceinline__ float exp_neg(float x) {
+  constexpr float kLog2e = 1.44269504088896341f, kLn2 = 0.693147180559945309f;
+  const float y = x < -150.0f ? -150.0f : x;
+  const float t = y * kLog2e, lo = __builtin_fmaf(y, kLog2e, -t);
+  const float e = __builtin_amdgcn_exp2f(t);
+  return __builtin_fmaf(e * kLn2, lo, e);
+}
+
+// A token's scores up to a common factor, from its logits z and their maximum m over the group:
+// exp(z - m), or sig(z) exp(-min(m, 0)) -- normalised sigmoid scores do not change by the factor,
+// and a token whose every logit is far below 0 keeps its digits. Without a finite logit they are 0
+// (a NaN stays one). shift is subtracted in the softmax's exponent (the backward's normaliser);
+// slope (when asked for) receives 1 - sig(z), without a cancellation.
+template <bool SIG, bool SLOPE, int NV>
+__device__ __forceinline__ void scores(float (&z)[NV], float m, float shift, float (&slope)[NV]) {
+  if (m == -INFINITY) {
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      z[i] = z[i] == -INFINITY ? 0.0f : z[i];
+      if constexpr (SLOPE) slope[i] = 0.0f;
+    }
+  } else if constexpr (!SIG) {
+#pragma unroll
+    for (int i = 0; i < NV; ++i) z[i] = exp_neg((z[i] - m) - shift);
+  } else {
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const float e = exp_neg(-fabsf(z[i])), d = __builtin_amdgcn_rcpf(1.0f + e);
+      if constexpr (SLOPE) slope[i] = z[i] > 0.0f ? e * d : d;
+      // with a logit above 0 the factor is 1: sig(z) = d or e d
+      z[i] = (m >= 0.0f ? (z[i] > 0.0f ? 1.0f : e) : exp_neg(z[i] - m)) * d;
+    }
+  }
 }
 
 // Segment bounds, clamped to the token range.
@@ -92,97 +125,154 @@ __device__ __forceinline__ int seg_of(const BalanceArgs& a, int64_t t) {
   return lo;
 }
 
-template <int VEC, int J>
-__global__ __launch_bounds__(kThreadsB) void balance_rows_kernel(BalanceArgs a, int G) {
+template <int NT>
+__device__ __forceinline__ double block_sum(double v, double* s_w) {
+  for (int o = 1; o < 64; o <<= 1) v += __shfl_xor(v, o);
+  __syncthreads();
+  if ((threadIdx.x & 63) == 0) s_w[threadIdx.x >> 6] = v;
+  __syncthreads();
+  v = 0.0;
+  for (int i = 0; i < NT / 64; ++i) v += s_w[i];
+  return v;
+}
+
+// The loss from the sum l of its segments' parts, the sum z of lse^2, and the segments' tokens.
+template <int NT>
+__device__ void finish_loss(const BalanceArgs& a, double l, double z, double* s_w) {
+  double n = 0.0, full = 0.0;
+  for (int i = threadIdx.x; i < a.S; i += NT) {
+    const int t = __hip_atomic_load(a.tokens + i, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    n += t;
+    full += t > 0;
+  }
+  l = block_sum<NT>(l, s_w);
+  z = block_sum<NT>(z, s_w);
+  n = block_sum<NT>(n, s_w);
+  full = block_sum<NT>(full, s_w);
+  if (threadIdx.x != 0) return;
+  a.loss[0] = full > 0.0 ? (float)((double)a.coef / full * l) : 0.0f;
+  a.loss[1] = n > 0.0 && a.zcoef != 0.0f ? (float)((double)a.zcoef / n * z) : 0.0f;
+  a.tokens[a.S] = (int)full;
+  a.tokens[a.S + 1] = (int)n;
+}
+
+// ALL: one workgroup takes every token and writes the results itself.
+template <int NT, bool ALL, bool SIG, int VEC, int J>
+__global__ __launch_bounds__(NT) void balance_rows_kernel(BalanceArgs a, int G) {
   constexpr int NV = VEC * J;
-  __shared__ float s_q[kThreadsB * NV];  // [groups][E]
+  constexpr int NW = NT / 64;
+  __shared__ float s_q[NW * (NV > 4 ? 1024 : 256)];  // [waves][E]; E <= 64 NV, and G >= E / 16
   __shared__ int s_c[1024];
   __shared__ int s_n;
-  __shared__ float s_z[kThreadsB / 64];
-  const int tid = threadIdx.x, g = tid / G, l = tid - g * G, groups = kThreadsB / G;
-  const int64_t c0 = (int64_t)blockIdx.x * a.rows, c1 = min(a.T, c0 + a.rows);
+  __shared__ double s_w[NT / 64];
+  const int tid = threadIdx.x, g = tid / G, l = tid - g * G, groups = NT / G;
+  const int64_t c0 = ALL ? 0 : (int64_t)blockIdx.x * a.rows, c1 = ALL ? a.T : min(a.T, c0 + a.rows);
   float zsum = 0.0f;
-  for (int s = seg_of(a, c0); s < a.S; ++s) {
+  double loss = 0.0;
+  if (!ALL && blockIdx.x == 0 && tid == 0) *a.done = 0;
+  for (int s = ALL ? 0 : seg_of(a, c0); s < a.S; ++s) {
     const int64_t s0 = seg_at(a, s), s1 = seg_at(a, s + 1);
-    if (s0 >= c1) break;
+    if (!ALL && s0 >= c1) break;
     const int64_t t0 = max(s0, c0), t1 = min(s1, c1);
-    if (t1 <= t0) continue;
-    for (int e = tid; e < a.E; e += kThreadsB) s_c[e] = 0;
+    if (!ALL && t1 <= t0) continue;
+    const auto counts = [&](int64_t t) { return t < t1 && (a.mask == nullptr || a.mask[t] != 0); };
+    float z[NV], zn[NV];  // this token's logits, the next one's
+    int64_t t = t0 + g;
+    bool on = counts(t);
+    if (on) load_row<VEC, J>(a.logits + t * a.E, a.E, l, G, -INFINITY, zn);
+    for (int e = tid; e < a.E; e += NT) s_c[e] = 0;
     if (tid == 0) s_n = 0;
     __syncthreads();
     // slots
     int n = 0;
-    for (int64_t i = t0 * a.k + tid; i < t1 * a.k; i += kThreadsB) {
-      const int64_t t = i / a.k;
-      if (a.mask != nullptr && a.mask[t] == 0) continue;
-      const int e = a.idx[i];
-      if (e >= 0 && e < a.E) atomicAdd(&s_c[e], 1);
-      n += t * a.k == i;
+    for (int64_t u = t0 + tid; u < t1; u += NT) {
+      if (!counts(u)) continue;
+      const int32_t* ids = a.idx + u * a.k;
+      for (int j = 0; j < a.k; ++j) {
+        const int e = ids[j];
+        if (e >= 0 && e < a.E) atomicAdd(&s_c[e], 1);
+      }
+      ++n;
     }
-    if (n != 0) atomicAdd(&s_n, n);
+    for (int o = 1; o < 64; o <<= 1) n += __shfl_xor(n, o);
+    if ((tid & 63) == 0 && n != 0) atomicAdd(&s_n, n);
     // scores
     float q[NV];
 #pragma unroll
     for (int i = 0; i < NV; ++i) q[i] = 0.0f;
-    for (int64_t b = t0; b < t1; b += groups) {
-      const int64_t t = b + g;
-      const bool on = t < t1 && (a.mask == nullptr || a.mask[t] != 0);
-      float z[NV];
+    for (int64_t b = t0; b < t1; b += groups, t += groups) {
+      const bool cur = on;
 #pragma unroll
-      for (int i = 0; i < NV; ++i) z[i] = 0.0f;
-      if (on) load_row<VEC, J>(a.logits + t * a.E, a.E, l, G, -INFINITY, z);
+      for (int i = 0; i < NV; ++i) z[i] = cur ? zn[i] : 0.0f;
+      on = counts(t + groups);
+      if (on) load_row<VEC, J>(a.logits + (t + groups) * a.E, a.E, l, G, -INFINITY, zn);
       float sum = 0.0f;
       float m = z[0];
 #pragma unroll
       for (int i = 1; i < NV; ++i) m = fmaxf(m, z[i]);
       m = lanes_max(m, G);
-      const bool none = m == -INFINITY;  // no finite logit: p = 0 (a NaN stays one)
-      const float top = fminf(m, 0.0f);
+      scores<SIG, false, NV>(z, m, 0.0f, z);
 #pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        z[i] = none ? (z[i] == -INFINITY ? 0.0f : z[i]) : (a.sigmoid ? scaled_sigmoid(z[i], top) : expf(z[i] - m));
-        sum += z[i];
-      }
+      for (int i = 0; i < NV; ++i) sum += z[i];
       sum = lanes_sum(sum, G);
-      if (a.sigmoid) {
-        if (on && l == 0) a.stat[t] = sum;
+      if constexpr (SIG) {
+        if (cur && l == 0) a.stat[t] = sum;
       } else {
         // stat is the log of the sum relative to the maximum: added to a large maximum it
         // would lose its digits, and the backward's scores with them
-        if (on && l == 0) {
+        if (cur && l == 0) {
           const float st = sum == 0.0f ? 0.0f : logf(sum), lse = m + st;
           a.stat[t] = st;
           if (sum != 0.0f) zsum = __builtin_fmaf(lse, lse, zsum);
         }
       }
-      const float inv = !on || sum == 0.0f ? 0.0f : 1.0f / sum;
-      if (on) {
+      const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+      if (cur) {
 #pragma unroll
         for (int i = 0; i < NV; ++i) q[i] = __builtin_fmaf(z[i], inv, q[i]);
       }
     }
+    // the groups of a wave, then the waves in order
 #pragma unroll
-    for (int j = 0; j < J; ++j)
+    for (int i = 0; i < NV; ++i)
+      for (int o = G; o < 64; o <<= 1) q[i] += __shfl_xor(q[i], o);
+    if ((tid & 63) < G) {
 #pragma unroll
-      for (int v = 0; v < VEC; ++v) {
-        const int e = (l + j * G) * VEC + v;
-        if (e < a.E) s_q[g * a.E + e] = q[j * VEC + v];
-      }
-    __syncthreads();
-    const int64_t at = (int64_t)blockIdx.x + s;
-    for (int e = tid; e < a.E; e += kThreadsB) {
-      float v = 0.0f;
-      for (int i = 0; i < groups; ++i) v += s_q[i * a.E + e];
-      a.wq[at * a.E + e] = v;
-      a.wc[at * a.E + e] = s_c[e];
+      for (int j = 0; j < J; ++j)
+#pragma unroll
+        for (int v = 0; v < VEC; ++v) {
+          const int e = (l + j * G) * VEC + v;
+          if (e < a.E) s_q[(tid >> 6) * a.E + e] = q[j * VEC + v];
+        }
     }
-    if (tid == 0) a.wn[at] = s_n;
+    __syncthreads();
+    const int ns = s_n;
+    for (int e = tid; e < a.E; e += NT) {
+      float v = 0.0f;
+#pragma unroll
+      for (int i = 0; i < NW; ++i) v += s_q[i * a.E + e];
+      if constexpr (ALL) {
+        a.counts[(int64_t)s * a.E + e] = s_c[e];
+        a.prob[(int64_t)s * a.E + e] = ns > 0 ? v / (float)ns : 0.0f;
+        if (ns > 0) loss += (double)s_c[e] * v * ((double)a.E / ((double)a.k * ns * ns));
+      } else {
+        const int64_t at = (int64_t)blockIdx.x + s;
+        a.wq[at * a.E + e] = v;
+        a.wc[at * a.E + e] = s_c[e];
+      }
+    }
+    if (tid == 0) {
+      if constexpr (ALL) a.tokens[s] = ns;
+      else a.wn[(int64_t)blockIdx.x + s] = ns;
+    }
     __syncthreads();
   }
-  zsum = lanes_sum(zsum, 64);
-  if ((tid & 63) == 0) s_z[tid >> 6] = zsum;
-  __syncthreads();
-  if (tid == 0) a.wz[blockIdx.x] = (s_z[0] + s_z[1]) + (s_z[2] + s_z[3]);
+  if constexpr (ALL) {
+    finish_loss<NT>(a, loss, zsum, s_w);
+  } else {
+    const double z = block_sum<NT>(zsum, s_w);
+    if (tid == 0) a.wz[blockIdx.x] = (float)z;
+  }
 }
 
 // Workgroup (64 experts, segment): wave w adds the partial rows w, w + 16, ... of the segment.
@@ -190,13 +280,15 @@ __global__ __launch_bounds__(1024) void balance_seg_kernel(BalanceArgs a) {
   __shared__ double s_q[16][64];
   __shared__ int s_c[16][64];
   __shared__ int s_n[16];
+  __shared__ double s_w[16];
+  __shared__ bool s_last;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, e = blockIdx.x * 64 + lane, s = blockIdx.y;
   const int64_t s0 = seg_at(a, s), s1 = seg_at(a, s + 1);
   const int lo = (int)(s0 / a.rows), hi = s1 > s0 ? (int)((s1 - 1) / a.rows) + 1 : lo;
   double q = 0.0;
   int c = 0, n = 0;
   if (e < a.E) {
-#pragma unroll 8
+#pragma unroll 16
     for (int i = lo + wave; i < hi; i += 16) {
       const int64_t at = ((int64_t)i + s) * a.E + e;
       q += (double)a.wq[at];
@@ -209,58 +301,41 @@ __global__ __launch_bounds__(1024) void balance_seg_kernel(BalanceArgs a) {
   s_c[wave][lane] = c;
   if (lane == 0) s_n[wave] = n;
   __syncthreads();
-  if (wave != 0) return;
-  q = 0.0;
-  c = n = 0;
-  for (int i = 0; i < 16; ++i) {
-    q += s_q[i][lane];
-    c += s_c[i][lane];
-    n += s_n[i];
+  if (wave == 0) {
+    q = 0.0;
+    c = n = 0;
+    for (int i = 0; i < 16; ++i) {
+      q += s_q[i][lane];
+      c += s_c[i][lane];
+      n += s_n[i];
+    }
+    double part = 0.0;
+    if (e < a.E) {
+      a.counts[(int64_t)s * a.E + e] = c;
+      a.prob[(int64_t)s * a.E + e] = n > 0 ? (float)(q / n) : 0.0f;
+      if (n > 0) part = (double)c * q * ((double)a.E / ((double)a.k * n * n));
+    }
+    for (int o = 1; o < 64; o <<= 1) part += __shfl_xor(part, o);
+    if (lane == 0) {
+      __hip_atomic_store(a.wl + (int64_t)s * gridDim.x + blockIdx.x, part, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+      if (blockIdx.x == 0) __hip_atomic_store(a.tokens + s, n, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+      // Both stores go past the XCD's L2 and have arrived before this workgroup is counted; the last
+      // one counted reads them all past its L2. (A release would write the whole L2 back: 5 us.)
+      asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+      const int parts = gridDim.x * gridDim.y;
+      s_last = __hip_atomic_fetch_add(a.done, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == parts - 1;
+    }
   }
-  double part = 0.0;
-  if (e < a.E) {
-    a.counts[(int64_t)s * a.E + e] = c;
-    a.prob[(int64_t)s * a.E + e] = n > 0 ? (float)(q / n) : 0.0f;
-    if (n > 0) part = (double)c * q * ((double)a.E / ((double)a.k * n * n));
-  }
-  for (int o = 1; o < 64; o <<= 1) part += __shfl_xor(part, o);
-  if (lane == 0) {
-    a.wl[(int64_t)s * gridDim.x + blockIdx.x] = part;
-    if (blockIdx.x == 0) a.tokens[s] = n;
-  }
-}
-
-__device__ __forceinline__ double block_sum_1024(double v, double* s_w) {
-  for (int o = 1; o < 64; o <<= 1) v += __shfl_xor(v, o);
   __syncthreads();
-  if ((threadIdx.x & 63) == 0) s_w[threadIdx.x >> 6] = v;
-  __syncthreads();
-  v = 0.0;
-  for (int i = 0; i < 16; ++i) v += s_w[i];
-  return v;
-}
-
-__global__ __launch_bounds__(1024) void balance_loss_kernel(BalanceArgs a, int parts) {
-  __shared__ double s_w[16];
-  double l = 0.0, z = 0.0, n = 0.0, full = 0.0;
-  for (int i = threadIdx.x; i < parts; i += 1024) l += a.wl[i];
+  if (!s_last) return;
+  double l = 0.0, z = 0.0;
+  for (int i = threadIdx.x; i < (int)(gridDim.x * gridDim.y); i += 1024)
+    l += __hip_atomic_load(a.wl + i, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
   for (int i = threadIdx.x; i < a.chunks; i += 1024) z += (double)a.wz[i];
-  for (int i = threadIdx.x; i < a.S; i += 1024) {
-    n += a.tokens[i];
-    full += a.tokens[i] > 0;
-  }
-  l = block_sum_1024(l, s_w);
-  z = block_sum_1024(z, s_w);
-  n = block_sum_1024(n, s_w);
-  full = block_sum_1024(full, s_w);
-  if (threadIdx.x != 0) return;
-  a.loss[0] = full > 0.0 ? (float)((double)a.coef / full * l) : 0.0f;
-  a.loss[1] = n > 0.0 && a.zcoef != 0.0f ? (float)((double)a.zcoef / n * z) : 0.0f;
-  a.tokens[a.S] = (int)full;
-  a.tokens[a.S + 1] = (int)n;
+  finish_loss<1024>(a, l, z, s_w);
 }
 
-template <typename TO, int VEC, int J>
+template <typename TO, bool SIG, int VEC, int J>
 __global__ __launch_bounds__(kThreadsB) void balance_grad_kernel(BalanceArgs a, int G, int64_t rows) {
   constexpr int NV = VEC * J;
   const int tid = threadIdx.x, g = tid / G, l = tid - g * G, groups = kThreadsB / G;
@@ -301,15 +376,13 @@ __global__ __launch_bounds__(kThreadsB) void balance_grad_kernel(BalanceArgs a, 
 #pragma unroll
       for (int i = 1; i < NV; ++i) m = fmaxf(m, z[i]);
       m = lanes_max(m, G);
-      const bool none = m == -INFINITY;
-      float dot = 0.0f;
-      if (a.sigmoid) {
-        const float inv = st == 0.0f ? 0.0f : 1.0f / st, top = fminf(m, 0.0f);
-        float slope[NV];
+      float dot = 0.0f, slope[NV];
+      scores<SIG, SIG, NV>(z, m, SIG ? 0.0f : st, slope);
+      if constexpr (SIG) {
+        const float inv = st == 0.0f ? 0.0f : 1.0f / st;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-          slope[i] = 0.0f;
-          z[i] = none ? (z[i] == -INFINITY ? 0.0f : z[i]) : scaled_sigmoid(z[i], top, &slope[i]) * inv;
+          z[i] *= inv;
           dot = __builtin_fmaf(z[i], c[i], dot);
         }
         dot = lanes_sum(dot, G);
@@ -317,12 +390,9 @@ __global__ __launch_bounds__(kThreadsB) void balance_grad_kernel(BalanceArgs a, 
         for (int i = 0; i < NV; ++i) z[i] = z[i] * slope[i] * (gs * (c[i] - dot));
       } else {
 #pragma unroll
-        for (int i = 0; i < NV; ++i) {
-          z[i] = none ? (z[i] == -INFINITY ? 0.0f : z[i]) : expf((z[i] - m) - st);
-          dot = __builtin_fmaf(z[i], c[i], dot);
-        }
+        for (int i = 0; i < NV; ++i) dot = __builtin_fmaf(z[i], c[i], dot);
         dot = lanes_sum(dot, G);
-        const float h = none || gz == 0.0f ? 0.0f : gz * (m + st);
+        const float h = m == -INFINITY || gz == 0.0f ? 0.0f : gz * (m + st);
 #pragma unroll
         for (int i = 0; i < NV; ++i) z[i] *= __builtin_fmaf(gs, c[i] - dot, h);
       }
@@ -368,14 +438,15 @@ void with_shape(const RowShape& r, F&& f) {
 
 BalanceWs balance_ws(int64_t T, int E, int S) {
   BalanceWs w;
-  w.rows = (int)std::max<int64_t>(16, (T + kBalanceChunks - 1) / kBalanceChunks);
-  w.chunks = (int)((T + w.rows - 1) / w.rows);
+  w.rows = (int)std::max<int64_t>(kBalanceRows, (T + kBalanceChunks - 1) / kBalanceChunks);
+  w.chunks = (int)std::max<int64_t>(1, (T + w.rows - 1) / w.rows);
   const size_t pairs = (size_t)w.chunks + S;
   size_t o = 0;
   w.q = o; o = up(o + 4 * pairs * E);
   w.c = o; o = up(o + 4 * pairs * E);
   w.n = o; o = up(o + 4 * pairs);
   w.z = o; o = up(o + 4 * (size_t)w.chunks);
+  w.done = o; o = up(o + 4);
   w.loss = o; o = up(o + 8 * (size_t)S * ((E + 63) / 64));
   w.bytes = o;
   return w;
@@ -383,14 +454,21 @@ BalanceWs balance_ws(int64_t T, int E, int S) {
 
 hipError_t launch_balance_fwd(const BalanceArgs& a, hipStream_t s) {
   const RowShape r = row_shape(a.E);
-  if (a.chunks > 0)
-    with_shape(r, [&](auto v, auto j) {
-      hipLaunchKernelGGL((balance_rows_kernel<decltype(v)::value, decltype(j)::value>), dim3(a.chunks), dim3(kThreadsB),
-                         0, s, a, r.G);
-    });
-  const int cg = (a.E + 63) / 64;
-  hipLaunchKernelGGL(balance_seg_kernel, dim3(cg, a.S), dim3(1024), 0, s, a);
-  hipLaunchKernelGGL(balance_loss_kernel, dim3(1), dim3(1024), 0, s, a, a.S * cg);
+  const bool all = a.T * a.E <= kBalanceSmall && a.S <= kBalanceSmallSegs;
+  with_shape(r, [&](auto v, auto j) {
+    constexpr int V = decltype(v)::value, JJ = decltype(j)::value;
+    const auto go = [&](auto sig) {
+      constexpr bool SIG = decltype(sig)::value;
+      if (all)
+        hipLaunchKernelGGL((balance_rows_kernel<1024, true, SIG, V, JJ>), dim3(1), dim3(1024), 0, s, a, r.G);
+      else
+        hipLaunchKernelGGL((balance_rows_kernel<kThreadsB, false, SIG, V, JJ>), dim3(a.chunks), dim3(kThreadsB), 0, s, a,
+                           r.G);
+    };
+    if (a.sigmoid) go(std::true_type());
+    else go(std::false_type());
+  });
+  if (!all) hipLaunchKernelGGL(balance_seg_kernel, dim3((a.E + 63) / 64, a.S), dim3(1024), 0, s, a);
   return hipGetLastError();
 }
 
@@ -402,10 +480,15 @@ hipError_t launch_balance_bwd(const BalanceArgs& a, hipStream_t s) {
   const int grid = (int)((a.T + rows - 1) / rows);
   with_shape(r, [&](auto v, auto j) {
     constexpr int V = decltype(v)::value, JJ = decltype(j)::value;
-    if (a.bf16_grad)
-      hipLaunchKernelGGL((balance_grad_kernel<bf16, V, JJ>), dim3(grid), dim3(kThreadsB), 0, s, a, r.G, rows);
-    else
-      hipLaunchKernelGGL((balance_grad_kernel<float, V, JJ>), dim3(grid), dim3(kThreadsB), 0, s, a, r.G, rows);
+    const auto go = [&](auto sig) {
+      constexpr bool SIG = decltype(sig)::value;
+      if (a.bf16_grad)
+        hipLaunchKernelGGL((balance_grad_kernel<bf16, SIG, V, JJ>), dim3(grid), dim3(kThreadsB), 0, s, a, r.G, rows);
+      else
+        hipLaunchKernelGGL((balance_grad_kernel<float, SIG, V, JJ>), dim3(grid), dim3(kThreadsB), 0, s, a, r.G, rows);
+    };
+    if (a.sigmoid) go(std::true_type());
+    else go(std::false_type());
   });
   return hipGetLastError();
 }

@@ -36,7 +36,7 @@ hipError_t launch_col_sum(const float* part, int P, int H, void* out, bool f32, 
 // rows, and the pairs that meet form a staircase, so c + s names the pair.
 struct BalanceWs {
   int chunks, rows;  // chunks of `rows` tokens
-  size_t q, c, n, z, loss, bytes;
+  size_t q, c, n, z, done, loss, bytes;
 };
 BalanceWs balance_ws(int64_t T, int E, int S);
 
@@ -59,6 +59,7 @@ struct BalanceArgs {
   int32_t* wc;         // [chunks + S][E] counts
   int32_t* wn;         // [chunks + S] tokens
   float* wz;           // [chunks] sums of lse^2
+  int32_t* done;       // workgroups of the second launch that are through
   double* wl;          // [S][ceil(E / 64)] parts of the loss
   const float* dloss;
   void* dlogits;
