@@ -8,6 +8,16 @@
 #include "mx.h"
 
 namespace mok {
+// Row stores of big arrays go past the caches, which could not keep them for a reader (more than
+// kNtBytes an output: 2048 x 7168 with MX rows 33 -> 25 us, 16384 x 7168 166 -> 159 us).
+constexpr int64_t kNtBytes = 16 << 20;
+
+template <bool NT>
+__device__ __forceinline__ void row_store(void* p, const uint4& v) {
+  typedef unsigned int u32x4_t __attribute__((ext_vector_type(4)));
+  if constexpr (NT) __builtin_nontemporal_store(u32x4_t{v.x, v.y, v.z, v.w}, reinterpret_cast<u32x4_t*>(p));
+  else stg16(p, v);
+}
 
 // Sum over a group of G lanes (a power of two up to 64, or whole waves of one workgroup),
 // in a fixed order; every lane gets it. s_red: one float per wave. All lanes of the
@@ -41,7 +51,7 @@ inline NormShape norm_shape(int H, int act) {
   return {(nv + 64 * vpt - 1) / (64 * vpt) * 64, 1, vpt};
 }
 
-template <typename T, int VPT, int Q>  // Q: 0 none, 1 MXFP8, 2 MXFP4
+template <typename T, int VPT, int Q, bool NT>  // Q: 0 none, 1 MXFP8, 2 MXFP4
 __global__ __launch_bounds__(1024) void norm_fwd_kernel(NormArgs a, int G) {
   constexpr int VE = Elem<T>::VE;
   __shared__ float s_red[16];
@@ -77,12 +87,12 @@ __global__ __launch_bounds__(1024) void norm_fwd_kernel(NormArgs a, int G) {
     const bool in = on && i < nv;
     float f[VE];
     if (in) {
-      if (a.r != nullptr) stg16((T*)a.r + base + i * VE, pack(v[j], (T*)nullptr));
+      if (a.r != nullptr) row_store<NT>((T*)a.r + base + i * VE, pack(v[j], (T*)nullptr));
       unpack(ldg16((const T*)a.w + i * VE), f, (T*)nullptr);
 #pragma unroll
       for (int e = 0; e < VE; ++e) f[e] = v[j][e] * rstd * f[e];
       const uint4 o = pack(f, (T*)nullptr);
-      if (a.y != nullptr) stg16((T*)a.y + base + i * VE, o);
+      if (a.y != nullptr) row_store<NT>((T*)a.y + base + i * VE, o);
       if constexpr (Q != 0) unpack(o, f, (T*)nullptr);  // the quantiser's input is the stored bf16 value
     }
     if constexpr (Q != 0) {
@@ -116,41 +126,44 @@ __global__ __launch_bounds__(1024) void norm_fwd_kernel(NormArgs a, int G) {
   }
 }
 
-template <typename T, int VPT>
+template <typename T, int VPT, bool NT>
 static void norm_fwd_q(const NormArgs& a, int quant, const NormShape& n, hipStream_t s) {
   const dim3 grid((unsigned)((a.T + n.rows - 1) / n.rows)), block(n.G * n.rows);
   if constexpr (std::is_same<T, bf16>::value) {
     if (quant == MOK_MXFP8) {
-      hipLaunchKernelGGL((norm_fwd_kernel<T, VPT, 1>), grid, block, 0, s, a, n.G);
+      hipLaunchKernelGGL((norm_fwd_kernel<T, VPT, 1, NT>), grid, block, 0, s, a, n.G);
       return;
     }
     if (quant == MOK_MXFP4) {
-      hipLaunchKernelGGL((norm_fwd_kernel<T, VPT, 2>), grid, block, 0, s, a, n.G);
+      hipLaunchKernelGGL((norm_fwd_kernel<T, VPT, 2, NT>), grid, block, 0, s, a, n.G);
       return;
     }
   }
-  hipLaunchKernelGGL((norm_fwd_kernel<T, VPT, 0>), grid, block, 0, s, a, n.G);
+  hipLaunchKernelGGL((norm_fwd_kernel<T, VPT, 0, NT>), grid, block, 0, s, a, n.G);
 }
 
-template <typename T>
+template <typename T, bool NT>
 static void norm_fwd_t(const NormArgs& a, int quant, const NormShape& n, hipStream_t s) {
-  if (n.vpt == 1) norm_fwd_q<T, 1>(a, quant, n, s);
-  else if (n.vpt == 2) norm_fwd_q<T, 2>(a, quant, n, s);
-  else if (n.vpt == 4) norm_fwd_q<T, 4>(a, quant, n, s);
-  else norm_fwd_q<T, 8>(a, quant, n, s);
+  if (n.vpt == 1) norm_fwd_q<T, 1, NT>(a, quant, n, s);
+  else if (n.vpt == 2) norm_fwd_q<T, 2, NT>(a, quant, n, s);
+  else if (n.vpt == 4) norm_fwd_q<T, 4, NT>(a, quant, n, s);
+  else norm_fwd_q<T, 8, NT>(a, quant, n, s);
 }
 
 hipError_t launch_norm_fwd(const NormArgs& a, int act, int quant, hipStream_t s) {
   const NormShape n = norm_shape(a.H, act);
-  if (act == MOK_F32) norm_fwd_t<float>(a, quant, n, s);
-  else norm_fwd_t<bf16>(a, quant, n, s);
+  const bool nt = a.T * a.H * (act == MOK_F32 ? 4 : 2) > kNtBytes;
+  if (act == MOK_F32) nt ? norm_fwd_t<float, true>(a, quant, n, s) : norm_fwd_t<float, false>(a, quant, n, s);
+  else nt ? norm_fwd_t<bf16, true>(a, quant, n, s) : norm_fwd_t<bf16, false>(a, quant, n, s);
   return hipGetLastError();
 }
 
 // Backward: a workgroup takes row groups blockIdx, blockIdx + grid, ... and keeps its columns'
 // share of dw in registers; the row groups of a workgroup are added in LDS in group order and
-// written as one partial row.
-template <typename T, int VPT>
+// written as one partial row. dr is loaded with dy and r, ahead of the row's sum (16384 x 7168:
+// 202 -> 172 us, 5.5 TB/s; the next row's loads ahead of the sum too: 265, its registers spill);
+// 512 workgroups, two per CU (768: 205 us, 1024: 180, 256: 321).
+template <typename T, int VPT, bool NT>
 __global__ __launch_bounds__(1024) void norm_bwd_kernel(NormArgs a, int G) {
   constexpr int VE = Elem<T>::VE;
   __shared__ float s_red[16];
@@ -167,6 +180,7 @@ __global__ __launch_bounds__(1024) void norm_bwd_kernel(NormArgs a, int G) {
     const bool on = t < a.T;
     const float rstd = on ? a.rstd[t] : 0.0f;
     float gv[VPT][VE], xh[VPT][VE];
+    uint4 dr[VPT];
     float c = 0.0f;
 #pragma unroll
     for (int j = 0; j < VPT; ++j) {
@@ -178,6 +192,7 @@ __global__ __launch_bounds__(1024) void norm_bwd_kernel(NormArgs a, int G) {
         unpack(ldg16((const T*)a.dy + base + i * VE), gv[j], (T*)nullptr);
         unpack(ldg16((const T*)a.r + base + i * VE), xh[j], (T*)nullptr);
         unpack(ldg16((const T*)a.w + i * VE), w, (T*)nullptr);
+        dr[j] = a.dr != nullptr ? ldg16((const T*)a.dr + base + i * VE) : make_uint4(0, 0, 0, 0);
 #pragma unroll
         for (int e = 0; e < VE; ++e) {
           xh[j][e] *= rstd;
@@ -193,15 +208,10 @@ __global__ __launch_bounds__(1024) void norm_bwd_kernel(NormArgs a, int G) {
       const int i = l + j * G;
       if (on && i < nv) {
         float f[VE];
-        if (a.dr != nullptr) {
-          unpack(ldg16((const T*)a.dr + base + i * VE), f, (T*)nullptr);
-        } else {
-#pragma unroll
-          for (int e = 0; e < VE; ++e) f[e] = 0.0f;
-        }
+        unpack(dr[j], f, (T*)nullptr);
 #pragma unroll
         for (int e = 0; e < VE; ++e) f[e] = __builtin_fmaf(rstd, gv[j][e] - xh[j][e] * c, f[e]);
-        stg16((T*)a.dx + base + i * VE, pack(f, (T*)nullptr));
+        row_store<NT>((T*)a.dx + base + i * VE, pack(f, (T*)nullptr));
       }
     }
   }
@@ -238,21 +248,22 @@ int norm_parts(int64_t T, int H, int act) {
   return (int)std::min<int64_t>(groups, 512);
 }
 
-template <typename T>
+template <typename T, bool NT>
 static void norm_bwd_t(const NormArgs& a, const NormShape& n, int grid, hipStream_t s) {
   const size_t lds = n.rows > 1 ? 4 * (size_t)n.rows * a.H : 0;
   const dim3 block(n.G * n.rows);
-  if (n.vpt == 1) hipLaunchKernelGGL((norm_bwd_kernel<T, 1>), dim3(grid), block, lds, s, a, n.G);
-  else if (n.vpt == 2) hipLaunchKernelGGL((norm_bwd_kernel<T, 2>), dim3(grid), block, lds, s, a, n.G);
-  else if (n.vpt == 4) hipLaunchKernelGGL((norm_bwd_kernel<T, 4>), dim3(grid), block, lds, s, a, n.G);
-  else hipLaunchKernelGGL((norm_bwd_kernel<T, 8>), dim3(grid), block, lds, s, a, n.G);
+  if (n.vpt == 1) hipLaunchKernelGGL((norm_bwd_kernel<T, 1, NT>), dim3(grid), block, lds, s, a, n.G);
+  else if (n.vpt == 2) hipLaunchKernelGGL((norm_bwd_kernel<T, 2, NT>), dim3(grid), block, lds, s, a, n.G);
+  else if (n.vpt == 4) hipLaunchKernelGGL((norm_bwd_kernel<T, 4, NT>), dim3(grid), block, lds, s, a, n.G);
+  else hipLaunchKernelGGL((norm_bwd_kernel<T, 8, NT>), dim3(grid), block, lds, s, a, n.G);
 }
 
 hipError_t launch_norm_bwd(const NormArgs& a, int act, hipStream_t s) {
   const NormShape n = norm_shape(a.H, act);
   const int grid = norm_parts(a.T, a.H, act);
-  if (act == MOK_F32) norm_bwd_t<float>(a, n, grid, s);
-  else norm_bwd_t<bf16>(a, n, grid, s);
+  const bool nt = a.T * a.H * (act == MOK_F32 ? 4 : 2) > kNtBytes;
+  if (act == MOK_F32) nt ? norm_bwd_t<float, true>(a, n, grid, s) : norm_bwd_t<float, false>(a, n, grid, s);
+  else nt ? norm_bwd_t<bf16, true>(a, n, grid, s) : norm_bwd_t<bf16, false>(a, n, grid, s);
   return hipGetLastError();
 }
 
