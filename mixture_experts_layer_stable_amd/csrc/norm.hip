@@ -20,19 +20,27 @@ __device__ __forceinline__ void row_store(void* p, const uint4& v) {
 }
 
 // Sum over a group of G lanes (a power of two up to 64, or whole waves of one workgroup),
-// in a fixed order; every lane gets it. s_red: one float per wave. All lanes of the
+// in a fixed order; every lane gets it. s_red: one per wave. All lanes of the
 // workgroup call it.
-__device__ __forceinline__ float group_sum(float v, int G, float* s_red) {
+template <typename V>
+__device__ __forceinline__ V group_sum(V v, int G, V* s_red) {
   const int w = G < 64 ? G : 64;
   for (int o = 1; o < w; o <<= 1) v += __shfl_xor(v, o);
   if (G <= 64) return v;
   const int wave = threadIdx.x >> 6, gw = G >> 6, w0 = wave / gw * gw;
   if ((threadIdx.x & 63) == 0) s_red[wave] = v;
   __syncthreads();
-  float t = 0.0f;
+  V t = 0;
   for (int i = 0; i < gw; ++i) t += s_red[w0 + i];
   __syncthreads();
   return t;
+}
+
+// 1 / sqrt(x) to half a step: the hardware's estimate and one Newton step on its exact residual.
+__device__ __forceinline__ float rsqrt_round(float x) {
+  const float r = __builtin_amdgcn_rsqf(x), h = x * r;
+  const float e = __builtin_fmaf(-h, r, 1.0f) - __builtin_fmaf(x, r, -h) * r;  // 1 - x r^2
+  return x > 0.0f && x < INFINITY ? __builtin_fmaf(0.5f * r, e, r) : r;
 }
 
 // Lanes per row, rows per workgroup and vectors per lane for rows of nv vectors: small rows
@@ -54,7 +62,7 @@ inline NormShape norm_shape(int H, int act) {
 template <typename T, int VPT, int Q, bool NT>  // Q: 0 none, 1 MXFP8, 2 MXFP4
 __global__ __launch_bounds__(1024) void norm_fwd_kernel(NormArgs a, int G) {
   constexpr int VE = Elem<T>::VE;
-  __shared__ float s_red[16];
+  __shared__ double s_red[16];
   const int g = threadIdx.x / G, l = threadIdx.x - g * G, nv = a.H / VE;
   const int64_t t = (int64_t)blockIdx.x * (blockDim.x / G) + g;
   const bool on = t < a.T;
@@ -78,8 +86,10 @@ __global__ __launch_bounds__(1024) void norm_fwd_kernel(NormArgs a, int G) {
 #pragma unroll
     for (int e = 0; e < VE; ++e) ss = __builtin_fmaf(v[j][e], v[j][e], ss);
   }
-  ss = group_sum(ss, G, s_red);
-  const float rstd = 1.0f / sqrtf(ss / (float)a.H + a.eps);
+  // An error of rstd moves a whole row, and with it every y next to a rounding border of bf16 or of
+  // the MX elements: the lanes' sums are added in fp64 and the root is right to half a step (of 14.7 M
+  // elements of y 75 are not the nearest bf16; the double rounding through fp32 alone gives 70).
+  const float rstd = rsqrt_round((float)(group_sum((double)ss, G, s_red) / a.H + (double)a.eps));
   if (on && l == 0 && a.rstd != nullptr) a.rstd[t] = rstd;
 #pragma unroll
   for (int j = 0; j < VPT; ++j) {
