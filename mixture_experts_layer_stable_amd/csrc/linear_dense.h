@@ -1,8 +1,8 @@
 // bf16 matrix product on direct global->LDS loads, for the products of linear.hip.
 //
 // A workgroup multiplies one BM x BN tile, each wave its part of it; both operands
-// of a 64-element K-tile arrive in one of two LDS stages by global_load_lds_dwordx4 (gemm2.h's
-// tile layouts, with ragged edges). With 256 x 256 tiles a SIMD holds one wave (256 fp32
+// of a 64-element K-tile arrive in LDS stages by global_load_lds_dwordx4 (gemm2.h's tile layouts,
+// with ragged edges). With 256 x 256 tiles a SIMD holds one wave (256 fp32
 // accumulators per lane), so nothing but the order of its own instructions hides its loads: every
 // LDS read and DMA of the loop has its place between two MFMAs (see dense_tile).
 #pragma once
@@ -147,78 +147,102 @@ struct DenseMN {
   }
 };
 
-// One K-tile from stage st (LDS offset lst), whose first fragments are in a[0], b[0]. A 16-k step
-// is NM MFMAs; behind each of its first ones goes a fragment read of the next step. At the last
-// step the wave holds every fragment that it needs of the stage: it waits for its own loads of
-// K-tile kt+1 and for the workgroup, then reads that tile's first fragments (from nx) and loads
-// kt+2's A into the stage that has become free, between the step's MFMAs; B follows in the first
-// step of the next K-tile, so the memory system sees two smaller bursts. sched_barrier keeps each
-// where it is put: left to itself the compiler gathers reads before the MFMAs (16384 x 4096 x 7168,
-// NT: 860 us, 810 placed; a wave's MFMA takes 32 cycles, room for its neighbour's few scalar and
-// address instructions). FULL: kt + 2 lies below both operands' full(), so no condition stays in
-// the loop (with conditions around the loads: 990 us).
-template <class Tl, bool FULL, class OA, class OB>
-__device__ __forceinline__ void dense_tile(const OA& oa, const OB& ob, int64_t kt, int64_t kt1, char* st, char* nx,
-                                           uint32_t lst, uint32_t lnx, int wave, uint4 (&a)[2][Tl::FM],
+// LDS stages: two of A, and of B two, or three where they fit the workgroup's share (256 x 256 tiles:
+// all 160 KB), whose third lets B be loaded a K-tile earlier.
+template <class OA, class OB, int BST>
+struct DenseRing {
+  static constexpr int BYTES = 2 * OA::BYTES + BST * OB::BYTES;
+  char* smem;
+  uint32_t lds;
+  int a0 = 0, b0 = 0;  // stages of the current K-tile
+  __device__ __forceinline__ int a_off(int d) const { return (a0 ^ (d & 1)) * OA::BYTES; }
+  __device__ __forceinline__ int b_off(int d) const {  // d < BST
+    const int q = b0 + d;
+    return 2 * OA::BYTES + (q >= BST ? q - BST : q) * OB::BYTES;
+  }
+  __device__ __forceinline__ void next() {
+    a0 ^= 1;
+    b0 = b0 + 1 == BST ? 0 : b0 + 1;
+  }
+};
+
+// One K-tile, whose first fragments are in a[0], b[0]. A 16-k step is NM MFMAs; behind each of its
+// first ones goes a fragment read of the next step. At the last step the wave holds every fragment
+// that it needs of the K-tile: it waits for its own loads of K-tile kt+1 and for the workgroup, then
+// reads that tile's first fragments and loads kt+2's A into the stage that has become free, between
+// the step's MFMAs. B's loads (of kt+2, or of kt+1 with two stages) go out in another step, so the
+// memory system sees two smaller bursts. sched_barrier keeps each where it is put: left to itself the
+// compiler gathers reads before the MFMAs (16384 x 4096 x 7168: 860 us, 810 placed; an MFMA takes 32
+// cycles, room for its neighbour's few scalar and address instructions). B's third stage: 748 ->
+// 738 us, 387 -> 379 for the weight gradient. FULL: kt + 2 lies below the operands' full(), so no
+// condition stays in the loop (with conditions around the loads: 990 us). 16 x 16 x 32 MFMAs need
+// twice the fragments, and spill.
+template <class Tl, bool FULL, int BST, class OA, class OB>
+__device__ __forceinline__ void dense_tile(const OA& oa, const OB& ob, int64_t kt, int64_t kt1,
+                                           const DenseRing<OA, OB, BST>& ring, int wave, uint4 (&a)[2][Tl::FM],
                                            uint4 (&b)[2][Tl::FN], f32x16_t (&acc)[Tl::FM][Tl::FN]) {
   constexpr int NM = Tl::FM * Tl::FN, NR = Tl::FM + Tl::FN, RS = (NR + NM - 1) / NM;
-  constexpr int HALF = NM > 1 ? NM / 2 : 1;  // MFMA slots that an operand's loads are spread over
-  const bool more1 = FULL || kt + 1 < kt1, more2 = FULL || kt + 2 < kt1;
+  constexpr int HALF = NM > 1 ? NM / 2 : 1;         // MFMA slots that an operand's loads are spread over
+  constexpr int BKS = BST == 3 ? 1 : 0, BS0 = BST == 3 ? 0 : NM / 4;  // step and slot of B's first load
+  const bool more1 = FULL || kt + 1 < kt1, more2 = FULL || kt + 2 < kt1, moreb = BST == 3 ? more2 : more1;
   static_for<0, 4>([&](auto kc) {
     constexpr int ks = decltype(kc)::value, c = ks & 1;
-    if constexpr (ks == 3) asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
-    const char* fr = ks == 3 ? nx : st;
+    if constexpr (ks == 3) {
+      if (BST == 3 && more2) wait_vmcnt<OB::NI>();  // all but B of kt+2
+      else wait_vmcnt<0>();
+      asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+    }
+    const char* fa = ring.smem + ring.a_off(ks == 3);
+    const char* fb = ring.smem + ring.b_off(ks == 3);
     static_for<0, NM>([&](auto ic) {
       constexpr int i = decltype(ic)::value;
       Mma<bf16>::run(acc[i / Tl::FN][i % Tl::FN], b[c][i % Tl::FN], a[c][i / Tl::FN]);
       if (ks < 3 || more1) {
         static_for<RS * i, (RS * (i + 1) < NR ? RS * (i + 1) : NR)>([&](auto rc) {
           constexpr int r = decltype(rc)::value;
-          if constexpr (r < Tl::FN) b[c ^ 1][r] = ob.frag(fr + OA::BYTES, r, (ks + 1) & 3);
-          else a[c ^ 1][r - Tl::FN] = oa.frag(fr, r - Tl::FN, (ks + 1) & 3);
+          if constexpr (r < Tl::FN) b[c ^ 1][r] = ob.frag(fb, r, (ks + 1) & 3);
+          else a[c ^ 1][r - Tl::FN] = oa.frag(fa, r - Tl::FN, (ks + 1) & 3);
         });
       }
-      constexpr int sa = i - (NM - HALF), sb = i - NM / 4;
+      constexpr int sa = i - (NM - HALF), sb = i - BS0;
       if constexpr (ks == 3 && sa >= 0)
-        if (more2) oa.template issue<FULL>(kt + 2, lst, wave, sa * OA::NI / HALF, (sa + 1) * OA::NI / HALF);
-      if constexpr (ks == 0 && sb >= 0 && sb < HALF)
-        if (more1)
-          ob.template issue<FULL>(kt + 1, lnx + OA::BYTES, wave, sb * OB::NI / HALF, (sb + 1) * OB::NI / HALF);
+        if (more2)
+          oa.template issue<FULL>(kt + 2, ring.lds + ring.a_off(0), wave, sa * OA::NI / HALF, (sa + 1) * OA::NI / HALF);
+      if constexpr (ks == BKS && sb >= 0 && sb < HALF)
+        if (moreb)
+          ob.template issue<FULL>(kt + BST - 1, ring.lds + ring.b_off(BST - 1), wave, sb * OB::NI / HALF,
+                                  (sb + 1) * OB::NI / HALF);
       __builtin_amdgcn_sched_barrier(0);
     });
   });
 }
 
-// acc += the products of K-tiles kt0 .. kt1-1 (kt1 > kt0). smem: two stages. The MFMA operands are
+// acc += the products of K-tiles kt0 .. kt1-1 (kt1 > kt0). smem: the ring. The MFMA operands are
 // swapped (transposed blocks): a lane then holds 16 columns of one row.
-template <class Tl, class OA, class OB>
+template <class Tl, int BST, class OA, class OB>
 __device__ __forceinline__ void dense_loop(const OA& oa, const OB& ob, int64_t kt0, int64_t kt1, char* smem, int wave,
                                            f32x16_t (&acc)[Tl::FM][Tl::FN]) {
-  constexpr int SB = OA::BYTES + OB::BYTES;
-  const uint32_t lds = lds_offset(smem);
-  oa.template issue<false>(kt0, lds, wave);
-  ob.template issue<false>(kt0, lds + OA::BYTES, wave);
+  DenseRing<OA, OB, BST> ring{smem, lds_offset(smem)};
+  oa.template issue<false>(kt0, ring.lds + ring.a_off(0), wave);
+  ob.template issue<false>(kt0, ring.lds + ring.b_off(0), wave);
   if (kt0 + 1 < kt1) {
-    oa.template issue<false>(kt0 + 1, lds + SB, wave);
-    wait_vmcnt<OA::NI>();
+    oa.template issue<false>(kt0 + 1, ring.lds + ring.a_off(1), wave);
+    if (BST == 3) ob.template issue<false>(kt0 + 1, ring.lds + ring.b_off(1), wave);
+    wait_vmcnt<OA::NI + (BST == 3 ? OB::NI : 0)>();
   } else {
     wait_vmcnt<0>();
   }
   ring_barrier();
   uint4 a[2][Tl::FM], b[2][Tl::FN];
 #pragma unroll
-  for (int fm = 0; fm < Tl::FM; ++fm) a[0][fm] = oa.frag(smem, fm, 0);
+  for (int fm = 0; fm < Tl::FM; ++fm) a[0][fm] = oa.frag(smem + ring.a_off(0), fm, 0);
 #pragma unroll
-  for (int fn = 0; fn < Tl::FN; ++fn) b[0][fn] = ob.frag(smem + OA::BYTES, fn, 0);
-  int cur = 0;
+  for (int fn = 0; fn < Tl::FN; ++fn) b[0][fn] = ob.frag(smem + ring.b_off(0), fn, 0);
   int64_t kt = kt0;
-  for (const int64_t full = min(kt1, oa.full()); kt + 2 < full; ++kt, cur ^= 1)
-    dense_tile<Tl, true>(oa, ob, kt, kt1, smem + cur * SB, smem + (cur ^ 1) * SB, lds + cur * SB,
-                         lds + (cur ^ 1) * SB, wave, a, b, acc);
+  for (const int64_t full = min(kt1, oa.full()); kt + 2 < full; ++kt, ring.next())
+    dense_tile<Tl, true, BST>(oa, ob, kt, kt1, ring, wave, a, b, acc);
 #pragma unroll 1
-  for (; kt < kt1; ++kt, cur ^= 1)
-    dense_tile<Tl, false>(oa, ob, kt, kt1, smem + cur * SB, smem + (cur ^ 1) * SB, lds + cur * SB,
-                          lds + (cur ^ 1) * SB, wave, a, b, acc);
+  for (; kt < kt1; ++kt, ring.next()) dense_tile<Tl, false, BST>(oa, ob, kt, kt1, ring, wave, a, b, acc);
   __syncthreads();
 }
 

@@ -17,7 +17,8 @@ __global__ __launch_bounds__(Tl::NT) void linear_dense_kernel(LinearArgs a) {
   using OA = std::conditional_t<KIND == LIN_DW, DenseMN<Tl::BM, Tl::FM, Tl::NW>, DenseK<Tl::BM, Tl::FM, Tl::NW>>;
   using OB = std::conditional_t<KIND == LIN_FWD, DenseK<Tl::BN, Tl::FN, Tl::NW, SW>, DenseMN<Tl::BN, Tl::FN, Tl::NW>>;
   constexpr int PATCH = Tl::NW * 32 * kDensePatch * 4;
-  constexpr int RING = 2 * (OA::BYTES + OB::BYTES);
+  constexpr int BST = Tl::BM * Tl::BN >= 256 * 256 ? 3 : 2;  // B's LDS stages
+  constexpr int RING = DenseRing<OA, OB, BST>::BYTES;
   __shared__ __align__(1024) char smem[RING > PATCH ? RING : PATCH];
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wm = wave / Tl::WN, wn = wave % Tl::WN;
@@ -55,7 +56,7 @@ __global__ __launch_bounds__(Tl::NT) void linear_dense_kernel(LinearArgs a) {
   }
   f32x16_t acc[Tl::FM][Tl::FN];
   zero_acc<Tl>(acc);
-  if (kt1 > kt0) dense_loop<Tl>(oa, ob, kt0, kt1, smem, wave, acc);
+  if (kt1 > kt0) dense_loop<Tl, BST>(oa, ob, kt0, kt1, smem, wave, acc);
 
   const auto in = [&](int row, int j) { return m0 + row < a.M && col(j) < a.N; };
   if constexpr (PART) {
