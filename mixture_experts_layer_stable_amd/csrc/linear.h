@@ -111,21 +111,26 @@ __device__ __forceinline__ void linear_bias8(const LinearArgs& a, int c, float (
   }
 }
 
-// out = f(sum of the slices' partial products + bias) + add: eight columns of a row per thread.
-// T: type of the operands.
-template <int KIND, int EPI, typename TO, typename T>
+// out = f(sum of the slices' partial products + bias) + add. A wave takes 64 / SL groups of eight
+// columns; SL lanes a group read every SL-th slice each and add their sums in a tree, so that few rows
+// do not wait for one slice after the other (5 x 4096 of 16 slices: 9.7 us with a lane for all of
+// them, 5.3 with 8). T: type of the operands.
+template <int KIND, int EPI, typename TO, typename T, int SL>
 __global__ __launch_bounds__(256) void linear_join_kernel(LinearArgs a) {
   constexpr bool SW = EPI == MOK_EPI_SWIGLU;
-  const int64_t nv = a.N / 8, i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (i >= a.M * nv) return;
-  const int64_t m = i / nv, P = SW ? 2 * a.N : a.N;
-  const int c = (int)(i - m * nv) * 8;
-  const Raw8<TO> add = linear_add8<TO>(a, m, c);
+  constexpr int CG = 64 / SL;
+  const int lane = threadIdx.x & 63, sl = lane / CG;
+  const int64_t nv = a.N / 8, i = ((int64_t)blockIdx.x * 4 + (threadIdx.x >> 6)) * CG + lane % CG;
+  const bool in = i < a.M * nv;
+  const int64_t m = in ? i / nv : 0, P = SW ? 2 * a.N : a.N;
+  const int c = in ? (int)(i - m * nv) * 8 : 0;
+  Raw8<TO> add{};
+  if (sl == 0) add = linear_add8<TO>(a, m, c);
   float g[8], u[8];
 #pragma unroll
   for (int q = 0; q < 8; ++q) g[q] = u[q] = 0.0f;
 #pragma unroll 4
-  for (int s = 0; s < a.split; ++s) {
+  for (int s = sl; s < a.split; s += SL) {
     const float* p = a.part + ((int64_t)s * a.M + m) * P + c;
     float v[8];
     load8(p, v);
@@ -137,8 +142,24 @@ __global__ __launch_bounds__(256) void linear_join_kernel(LinearArgs a) {
       for (int q = 0; q < 8; ++q) u[q] += v[q];
     }
   }
+#pragma unroll
+  for (int o = CG; o < 64; o <<= 1)
+#pragma unroll
+    for (int q = 0; q < 8; ++q) {
+      g[q] += __shfl_xor(g[q], o);
+      if constexpr (SW) u[q] += __shfl_xor(u[q], o);
+    }
+  if (!in || sl != 0) return;
   if constexpr (KIND == LIN_FWD) linear_bias8<EPI>(a, c, g, u);
   linear_store8<KIND, EPI, TO, T>(a, m, c, g, u, add);
+}
+
+template <int KIND, int EPI, typename TO, typename T>
+inline void linear_join(const LinearArgs& a, hipStream_t s) {
+  const int64_t groups = a.M * (a.N / 8);
+  const auto grid = [&](int sl) { return dim3((unsigned)((groups * sl + 255) / 256)); };
+  if (a.split >= 8) hipLaunchKernelGGL((linear_join_kernel<KIND, EPI, TO, T, 8>), grid(8), dim3(256), 0, s, a);
+  else hipLaunchKernelGGL((linear_join_kernel<KIND, EPI, TO, T, 2>), grid(2), dim3(256), 0, s, a);
 }
 
 }  // namespace mok

@@ -134,8 +134,7 @@ void run_simple(const LinearArgs& a, hipStream_t s) {
   }
   hipLaunchKernelGGL((linear_simple_kernel<Tile, float, KIND, SW ? MOK_EPI_SWIGLU : MOK_EPI_NONE, float, true>), grid,
                      dim3(256), 0, s, a);
-  hipLaunchKernelGGL((linear_join_kernel<KIND, EPI, float, float>), dim3((unsigned)((a.M * (a.N / 8) + 255) / 256)),
-                     dim3(256), 0, s, a);
+  linear_join<KIND, EPI, float, float>(a, s);
 }
 
 template <class Tile>
@@ -222,7 +221,7 @@ void run_dpre(const void* dy, const void* pre, int64_t M, int N, int epi, void* 
 // The plan of least estimated time. A tile's time is its K-tiles times what one takes (half as long
 // on an empty chip as on a full one), plus a fixed part (first loads, epilogue); the tiles go out in
 // rounds of as many as fit the 256 CUs. Slices of K cost their fp32 partial products' way to memory
-// and back, and a second launch that reads them one after the other. The constants (us) are fitted
+// and back, and a second launch. The constants (us) are fitted
 // to 28 shapes from 1 to 16384 rows at every tile and split: the plan taken is the fastest or within
 // a tenth of it.
 LinearPlan linear_plan(int kind, int act, int epi, int64_t M, int N, int64_t K) {
@@ -247,7 +246,7 @@ LinearPlan linear_plan(int kind, int act, int epi, int64_t M, int N, int64_t K) 
       const double rounds = (double)((tiles * split + slots - 1) / slots);
       const double fill = std::min(1.0, (double)(tiles * split) / (double)slots);
       double us = rounds * ((double)((kt + split - 1) / split) * c.ktile * (0.5 + 0.5 * fill) + c.fixed);
-      if (split > 1) us += 4.0 + 0.25 * split + 8.0 * split * (double)M * (double)P / 4e6;
+      if (split > 1) us += 5.0 + 8.0 * split * (double)M * (double)P / 4e6;
       if (us < least) {
         least = us;
         best = {t, split};

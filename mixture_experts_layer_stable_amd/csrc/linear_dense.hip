@@ -109,8 +109,7 @@ void run(const LinearArgs& a, hipStream_t s) {
   }
   hipLaunchKernelGGL((linear_dense_kernel<Tl, KIND, SW ? MOK_EPI_SWIGLU : MOK_EPI_NONE, bf16, true>), grid, block, 0, s,
                      a);
-  hipLaunchKernelGGL((linear_join_kernel<KIND, EPI, TO, bf16>), dim3((unsigned)((a.M * (a.N / 8) + 255) / 256)), dim3(256), 0,
-                     s, a);
+  linear_join<KIND, EPI, TO, bf16>(a, s);
 }
 
 template <class Tl>
