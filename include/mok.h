@@ -443,7 +443,7 @@ mok_status mok_rmsnorm_forward(const mok_norm_desc* d, const void* x, const void
  *   g = dy * w:  dx = dr + rstd * (g - xh * mean_h(g * xh))  (the gradient of x and of res),
  *   dw_h = sum_t dy * xh.
  * r [T][H] and rstd [T] as the forward wrote them (r = x without a residual); dr may be NULL
- * (0).  dx [T][H] may be the same array as dy or dr.  dw [H] in act (fp32 with
+ * (0).  dx [T][H] may be the same array as dy or dr (not as r).  dw [H] in act (fp32 with
  * MOK_FLAG_WGRAD_F32) may be NULL; every element is written (zero for T = 0).  ws is used
  * (and required) only with dw.
  */
@@ -512,8 +512,8 @@ mok_status mok_balance_backward(const mok_balance_desc* d, const float* logits, 
  * Matrix product with bias, activation and residual in its epilogue, and its gradients: the
  * dense (shared) expert beside the routed ones, its second product with the layer's y as the
  * residual, and the product that takes the gradient of the router's logits into dx and dWr.
- *   M rows (0 <= M < 2^31), K inputs, N outputs: N, K multiples of 8, 8 .. 2^20, every matrix
- *   below 2^38 elements (MOK_ERR_SHAPE).
+ *   M rows (0 <= M < 2^30), K inputs, N outputs: N, K multiples of 8, 8 .. 2^20, every matrix
+ *   below 2^37 elements (MOK_ERR_SHAPE).
  *   act: MOK_F32 or MOK_BF16, the type of x, w, res, y, pre, dy, dx and dx_add.
  *   epi, with P = 2N for MOK_EPI_SWIGLU and P = N else:
  *     MOK_EPI_NONE   f(p) = p             MOK_EPI_SILU  f(p) = p sig(p)
@@ -548,7 +548,7 @@ mok_status mok_linear_workspace_query(const mok_linear_desc* d, mok_linear_sizes
 /*
  * mok_linear_forward -- p = x w^T + bias;  y = f(p) + res, in fp32, rounded once.
  * x [M][K], w [P][K], bias [P] fp32 or NULL, res [M][N] or NULL (may be the same array as
- * y), y [M][N], pre [M][P] (p, for the backward) or NULL.
+ * y), y [M][N], pre [M][P] (p, for the backward) or NULL.  No other overlap is allowed.
  */
 mok_status mok_linear_forward(const mok_linear_desc* d, const void* x, const void* w, const float* bias,
                               const void* res, void* y, void* pre, void* ws, size_t ws_bytes, void* stream);
@@ -559,7 +559,8 @@ mok_status mok_linear_forward(const mok_linear_desc* d, const void* x, const voi
  *   dx = dp w + dx_add,  dw = dp^T x + dw_add,  db = sum_m dp  (before that rounding),
  * each summed in fp32 and rounded once.  dx [M][K], dw [P][K] and db [P] fp32 may be NULL:
  * that gradient is then not formed (w is read for dx only, x for dw only).  dx_add, dw_add
- * (of dx's and dw's shape and type) may be NULL and may be the same arrays as dx and dw.
+ * (of dx's and dw's shape and type) may be NULL and may be the same arrays as dx and dw; no
+ * other overlap is allowed.
  * dw and db are written for M = 0 too (dw_add or 0, and 0).  The gradient by res is dy.
  */
 mok_status mok_linear_backward(const mok_linear_desc* d, const void* dy, const void* pre, const void* x, const void* w,

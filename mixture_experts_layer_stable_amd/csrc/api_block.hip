@@ -55,12 +55,12 @@ mok_status check_linear(const mok_linear_desc* d) {
   if (d->act != MOK_F32 && d->act != MOK_BF16) return MOK_ERR_DTYPE;
   if (d->epi < MOK_EPI_NONE || d->epi > MOK_EPI_SWIGLU) return MOK_ERR_DTYPE;
   if (d->reserved != 0 || (d->flags & ~MOK_FLAG_WGRAD_F32) != 0) return MOK_ERR_SHAPE;
-  if (d->M < 0 || d->M >= ((int64_t)1 << 31)) return MOK_ERR_SHAPE;
+  if (d->M < 0 || d->M >= ((int64_t)1 << 30)) return MOK_ERR_SHAPE;
   if (d->N < 8 || d->N > (1 << 20) || d->N % 8 != 0) return MOK_ERR_SHAPE;
   if (d->K < 8 || d->K > (1 << 20) || d->K % 8 != 0) return MOK_ERR_SHAPE;
-  // any array past 2^38 elements is larger than the GPU's memory; output tiles fit 32 bits
+  // an array of 2^37 elements is as large as the GPU's memory; the output tiles' threads fit 32 bits
   const int64_t P = d->epi == MOK_EPI_SWIGLU ? 2LL * d->N : d->N;
-  if (std::max<int64_t>(d->M, 1) * std::max<int64_t>(P, d->K) >= (1LL << 38) || P * d->K >= (1LL << 38))
+  if (std::max<int64_t>(d->M, 1) * std::max<int64_t>(P, d->K) >= (1LL << 37) || P * d->K >= (1LL << 37))
     return MOK_ERR_SHAPE;
   return MOK_OK;
 }

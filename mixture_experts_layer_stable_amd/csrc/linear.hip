@@ -241,8 +241,9 @@ LinearPlan linear_plan(int kind, int act, int epi, int64_t M, int N, int64_t K) 
   for (int t = 0; t < (f32 ? 2 : 4); ++t) {
     const Tile& c = f32 ? (epi == MOK_EPI_SWIGLU ? kTilesF32Sw[t] : kTilesF32[t]) : kTiles[t];
     const int64_t tiles = ((M + c.bm - 1) / c.bm) * ((P + c.bn - 1) / c.bn), slots = 256 * c.per_cu;
-    for (int split = 1; split <= 32; split *= 2) {
-      if (split > 1 && kt / split < 2) break;
+    if (t > 0 && tiles >= (1 << 23)) continue;  // 2^32 threads a launch; the largest tile always fits
+    for (int split = 1; split <= 256; split *= 2) {
+      if (split > 1 && (kt / split < 2 || tiles * split >= (1 << 16))) break;
       const double rounds = (double)((tiles * split + slots - 1) / slots);
       const double fill = std::min(1.0, (double)(tiles * split) / (double)slots);
       double us = rounds * ((double)((kt + split - 1) / split) * c.ktile * (0.5 + 0.5 * fill) + c.fixed);

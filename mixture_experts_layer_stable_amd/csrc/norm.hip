@@ -64,73 +64,76 @@ __global__ __launch_bounds__(1024) void norm_fwd_kernel(NormArgs a, int G) {
   constexpr int VE = Elem<T>::VE;
   __shared__ double s_red[16];
   const int g = threadIdx.x / G, l = threadIdx.x - g * G, nv = a.H / VE;
-  const int64_t t = (int64_t)blockIdx.x * (blockDim.x / G) + g;
-  const bool on = t < a.T;
-  const int64_t base = t * a.H;
-  float v[VPT][VE];
-  float ss = 0.0f;
+  const int rows = blockDim.x / G;
+  for (int64_t t0 = (int64_t)blockIdx.x * rows; t0 < a.T; t0 += (int64_t)gridDim.x * rows) {
+    const int64_t t = t0 + g;
+    const bool on = t < a.T;
+    const int64_t base = t * a.H;
+    float v[VPT][VE];
+    float ss = 0.0f;
 #pragma unroll
-  for (int j = 0; j < VPT; ++j) {
-    const int i = l + j * G;
+    for (int j = 0; j < VPT; ++j) {
+      const int i = l + j * G;
 #pragma unroll
-    for (int e = 0; e < VE; ++e) v[j][e] = 0.0f;
-    if (on && i < nv) {
-      unpack(ldg16((const T*)a.x + base + i * VE), v[j], (T*)nullptr);
-      if (a.res != nullptr) {
-        float f[VE];
-        unpack(ldg16((const T*)a.res + base + i * VE), f, (T*)nullptr);
+      for (int e = 0; e < VE; ++e) v[j][e] = 0.0f;
+      if (on && i < nv) {
+        unpack(ldg16((const T*)a.x + base + i * VE), v[j], (T*)nullptr);
+        if (a.res != nullptr) {
+          float f[VE];
+          unpack(ldg16((const T*)a.res + base + i * VE), f, (T*)nullptr);
 #pragma unroll
-        for (int e = 0; e < VE; ++e) v[j][e] += f[e];
-      }
-    }
-#pragma unroll
-    for (int e = 0; e < VE; ++e) ss = __builtin_fmaf(v[j][e], v[j][e], ss);
-  }
-  // An error of rstd moves a whole row, and with it every y next to a rounding border of bf16 or of
-  // the MX elements: the lanes' sums are added in fp64 and the root is right to half a step (of 14.7 M
-  // elements of y 75 are not the nearest bf16; the double rounding through fp32 alone gives 70).
-  const float rstd = rsqrt_round((float)(group_sum((double)ss, G, s_red) / a.H + (double)a.eps));
-  if (on && l == 0 && a.rstd != nullptr) a.rstd[t] = rstd;
-#pragma unroll
-  for (int j = 0; j < VPT; ++j) {
-    const int i = l + j * G;
-    const bool in = on && i < nv;
-    float f[VE];
-    if (in) {
-      if (a.r != nullptr) row_store<NT>((T*)a.r + base + i * VE, pack(v[j], (T*)nullptr));
-      unpack(ldg16((const T*)a.w + i * VE), f, (T*)nullptr);
-#pragma unroll
-      for (int e = 0; e < VE; ++e) f[e] = v[j][e] * rstd * f[e];
-      const uint4 o = pack(f, (T*)nullptr);
-      if (a.y != nullptr) row_store<NT>((T*)a.y + base + i * VE, o);
-      if constexpr (Q != 0) unpack(o, f, (T*)nullptr);  // the quantiser's input is the stored bf16 value
-    }
-    if constexpr (Q != 0) {
-      // H is a multiple of 128: the 16 lanes of a K-tile (four blocks of four lanes) are all
-      // in or all out of the row
-      float m = 0.0f;
-      if (in) {
-#pragma unroll
-        for (int e = 0; e < VE; ++e) m = fmaxf(m, fabsf(f[e]));
-      }
-      m = fmaxf(m, __shfl_xor(m, 1));
-      m = fmaxf(m, __shfl_xor(m, 2));
-      const uint32_t sb = Q == 1 ? mx_scale_byte(m) : mx4_scale_byte(m);
-      const float inv = mx_inv_scale(sb);
-      uint32_t sw = sb << (8 * ((l >> 2) & 3));
-      sw |= __shfl_xor(sw, 4);
-      sw |= __shfl_xor(sw, 8);
-      if (in) {
-        if constexpr (Q == 1) {
-          *reinterpret_cast<uint2*>(a.q + base + i * VE) =
-              make_uint2(mx_pack4(f[0], f[1], f[2], f[3], inv), mx_pack4(f[4], f[5], f[6], f[7], inv));
-        } else {
-          uint32_t w = 0;
-#pragma unroll
-          for (int e = 0; e < VE; ++e) w |= e2m1_code(f[e] * inv) << (4 * e);
-          *reinterpret_cast<uint32_t*>(a.q + (base + i * VE) / 2) = w;
+          for (int e = 0; e < VE; ++e) v[j][e] += f[e];
         }
-        if ((i & 15) == 0) *reinterpret_cast<uint32_t*>(a.s + ((int64_t)(i >> 4) * a.T + t) * 4) = sw;
+      }
+#pragma unroll
+      for (int e = 0; e < VE; ++e) ss = __builtin_fmaf(v[j][e], v[j][e], ss);
+    }
+    // An error of rstd moves a whole row, and with it every y next to a rounding border of bf16 or of
+    // the MX elements: the lanes' sums are added in fp64 and the root is right to half a step (of 14.7 M
+    // elements of y 75 are not the nearest bf16; the double rounding through fp32 alone gives 70).
+    const float rstd = rsqrt_round((float)(group_sum((double)ss, G, s_red) / a.H + (double)a.eps));
+    if (on && l == 0 && a.rstd != nullptr) a.rstd[t] = rstd;
+#pragma unroll
+    for (int j = 0; j < VPT; ++j) {
+      const int i = l + j * G;
+      const bool in = on && i < nv;
+      float f[VE];
+      if (in) {
+        if (a.r != nullptr) row_store<NT>((T*)a.r + base + i * VE, pack(v[j], (T*)nullptr));
+        unpack(ldg16((const T*)a.w + i * VE), f, (T*)nullptr);
+#pragma unroll
+        for (int e = 0; e < VE; ++e) f[e] = v[j][e] * rstd * f[e];
+        const uint4 o = pack(f, (T*)nullptr);
+        if (a.y != nullptr) row_store<NT>((T*)a.y + base + i * VE, o);
+        if constexpr (Q != 0) unpack(o, f, (T*)nullptr);  // the quantiser's input is the stored bf16 value
+      }
+      if constexpr (Q != 0) {
+        // H is a multiple of 128: the 16 lanes of a K-tile (four blocks of four lanes) are all
+        // in or all out of the row
+        float m = 0.0f;
+        if (in) {
+#pragma unroll
+          for (int e = 0; e < VE; ++e) m = fmaxf(m, fabsf(f[e]));
+        }
+        m = fmaxf(m, __shfl_xor(m, 1));
+        m = fmaxf(m, __shfl_xor(m, 2));
+        const uint32_t sb = Q == 1 ? mx_scale_byte(m) : mx4_scale_byte(m);
+        const float inv = mx_inv_scale(sb);
+        uint32_t sw = sb << (8 * ((l >> 2) & 3));
+        sw |= __shfl_xor(sw, 4);
+        sw |= __shfl_xor(sw, 8);
+        if (in) {
+          if constexpr (Q == 1) {
+            *reinterpret_cast<uint2*>(a.q + base + i * VE) =
+                make_uint2(mx_pack4(f[0], f[1], f[2], f[3], inv), mx_pack4(f[4], f[5], f[6], f[7], inv));
+          } else {
+            uint32_t w = 0;
+#pragma unroll
+            for (int e = 0; e < VE; ++e) w |= e2m1_code(f[e] * inv) << (4 * e);
+            *reinterpret_cast<uint32_t*>(a.q + (base + i * VE) / 2) = w;
+          }
+          if ((i & 15) == 0) *reinterpret_cast<uint32_t*>(a.s + ((int64_t)(i >> 4) * a.T + t) * 4) = sw;
+        }
       }
     }
   }
@@ -138,7 +141,8 @@ __global__ __launch_bounds__(1024) void norm_fwd_kernel(NormArgs a, int G) {
 
 template <typename T, int VPT, bool NT>
 static void norm_fwd_q(const NormArgs& a, int quant, const NormShape& n, hipStream_t s) {
-  const dim3 grid((unsigned)((a.T + n.rows - 1) / n.rows)), block(n.G * n.rows);
+  // a workgroup a row group, up to the 2^32 threads that a launch can have
+  const dim3 grid((unsigned)std::min<int64_t>((a.T + n.rows - 1) / n.rows, 1 << 21)), block(n.G * n.rows);
   if constexpr (std::is_same<T, bf16>::value) {
     if (quant == MOK_MXFP8) {
       hipLaunchKernelGGL((norm_fwd_kernel<T, VPT, 1, NT>), grid, block, 0, s, a, n.G);

@@ -221,6 +221,35 @@ def test_no_tokens():
         assert loss.tolist() == [0, 0] and (counts == 0).all() and (tokens == 0).all() and (prob == 0).all()
 
 
+@pytest.mark.gpu
+def test_offsets_past_32_bits():
+    T, E, k = (1 << 22) + 5, 516, 2
+    z = torch.zeros(T, E, device=DEV)
+    z[:, 3], z[-1, 7], z[T // 2, 9] = 1.0, 4.0, 5.0
+    idx = torch.zeros(T, k, dtype=torch.int32, device=DEV)
+    idx[:, 1] = 3
+    idx[-1, 0] = 515
+    dl = torch.tensor([1e9, 0.0], device=DEV)   # a gradient of T tokens, in fp32's range
+    mok = _mok()
+    d = mok.BalanceDesc(T, E, k)
+    f, i32 = (lambda *s: torch.empty(*s, device=DEV)), torch.int32
+    loss, counts, tokens, prob, stat, dz = f(2), f(1, E).to(i32), f(3).to(i32), f(1, E), f(T), f(T, E)
+    ws = torch.empty(mok.balance_workspace_query(d)["fwd_ws"], dtype=torch.uint8, device=DEV)
+    mok.balance_forward(d, z, idx, loss, counts, tokens, prob, stat, ws)
+    mok.balance_backward(d, z, counts, tokens, stat, dl, dz)
+    c = torch.zeros(E, dtype=torch.float64, device=DEV)
+    c[0], c[3], c[515] = T - 1, T, 1
+    assert torch.equal(counts[0].double(), c) and tokens.tolist() == [T, 1, T]
+    rows = torch.tensor([0, 1, T // 2, T - 2, T - 1], device=DEV)
+    p = torch.softmax(z[rows].double(), 1)
+    want = 1e9 * E / (k * float(T) ** 2) * p * (c - (p * c).sum(1, keepdim=True))
+    size = 1e9 * E / (k * float(T) ** 2) * p * (c + (p * c).sum(1, keepdim=True))
+    assert ((dz[rows].double() - want).abs() <= 2.0**-18 * size).all()
+    base = torch.softmax(z[0].double(), 0)
+    # every lane adds T/1024/16 rows' equal p in fp32
+    assert ((prob[0].double() - base).abs() <= (2.0**-20 + T / 16384 * 2.0**-24) * base + 2.0 / T).all()
+
+
 # ---- refusals (no GPU needed) ----
 
 @pytest.mark.parametrize("kw,status", [

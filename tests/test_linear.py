@@ -249,6 +249,36 @@ def test_no_rows():
     assert (c.backward(add=False)[1] == 0).all()
 
 
+@pytest.mark.gpu
+@pytest.mark.parametrize("act", ["bf16", "f32"])
+def test_offsets_past_32_bits(act):
+    """Rows whose elements lie past 2^31 of x, y and dx, and a weight gradient over all of them."""
+    mok = _mok()
+    t = mok.TORCH_DTYPE[mok.DTYPES[act]]
+    M, N, K = (1 << 27) + 77, 24, 24
+    print("case linear large", M, N, K, act, flush=True)
+    g = torch.Generator(device=DEV).manual_seed(5)
+    x = torch.empty(M, K, dtype=t, device=DEV).normal_(generator=g)
+    w = torch.randn(N, K, generator=g, device=DEV).to(t)
+    d = mok.LinearDesc(M, N, K, act=mok.DTYPES[act], flags=mok.FLAG_WGRAD_F32)
+    sz = mok.linear_workspace_query(d)
+    ws = torch.empty(max(sz["fwd_ws"], sz["bwd_ws"], 16), dtype=torch.uint8, device=DEV)
+    y, dw = torch.empty(M, N, dtype=t, device=DEV), torch.empty(N, K, device=DEV)
+    mok.linear_forward(d, x, w, y, ws=ws)
+    for sl in (slice(0, 300), slice(M // 2, M // 2 + 300), slice(M - 300, M)):
+        near(y[sl], (x[sl].double() @ w.double().t()).cpu(), 24 * 2.0**-24 * (x[sl].double().abs() @ w.double().abs().t()).cpu(), "y")
+    x[:] = 0            # the weight gradient of a few rows at both ends
+    x[5], x[-3] = 1.0, 2.0
+    y[:] = 0
+    y[5, 1], y[-3, 2] = 3.0, 4.0
+    mok.linear_backward(d, y, x, w, dw=dw, ws=ws)
+    want = torch.zeros(N, K, device=DEV)
+    want[1], want[2] = 3.0, 8.0
+    assert torch.equal(dw, want)
+    mok.linear_backward(d, y, x, w, dx=x, ws=ws)   # x itself is not read for dx
+    assert torch.equal(x[-3].double(), (4 * w[2].double()).to(t).double()) and (x[:5] == 0).all() and (x[-2:] == 0).all()
+
+
 # ---- refusals (no GPU needed) ----
 
 @pytest.mark.parametrize("kw,status", [

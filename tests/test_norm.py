@@ -267,6 +267,34 @@ def test_empty_batch_and_flags():
     assert torch.equal(dx, dx2)
 
 
+@pytest.mark.gpu
+@pytest.mark.parametrize("T,H", [((1 << 25) + 37, 8), ((1 << 18) + 3, 8200)])
+def test_more_rows_than_workgroups_and_offsets_past_32_bits(T, H):
+    mok = _mok()
+    print("case norm large", T, H, flush=True)
+    g = torch.Generator(device=DEV).manual_seed(1)
+    x = torch.empty(T, H, dtype=torch.bfloat16, device=DEV).normal_(generator=g)
+    w = (1 + 0.1 * torch.randn(H, device=DEV, generator=g)).bfloat16()
+    d = mok.NormDesc(T, H, eps=1e-5)
+    y, rstd = torch.empty_like(x), torch.empty(T, device=DEV)
+    mok.rmsnorm_forward(d, x, w, y=y, rstd=rstd)
+    for sl in (slice(0, 100), slice(T // 2, T // 2 + 100), slice(T - 100, T)):
+        _close(y[sl], _reference(x[sl], None, w, 1e-5)[2])
+        _close(rstd[sl], _reference(x[sl], None, w, 1e-5)[1])
+    dx, dw = torch.empty_like(x), torch.empty_like(w)
+    ws = torch.empty(mok.norm_workspace_query(d)["bwd_ws"], dtype=torch.uint8, device=DEV)
+    mok.rmsnorm_backward(d, y, x, w, rstd, dx, dw=dw, ws=ws)
+    for sl in (slice(0, 100), slice(T - 100, T)):
+        xh, gv = x[sl].double() * rstd[sl].double()[:, None], y[sl].double() * w.double()
+        size = rstd[sl].double()[:, None] * (gv.abs() + xh.abs() * (gv * xh).abs().mean(-1, keepdim=True))
+        _close(dx[sl], rstd[sl].double()[:, None] * (gv - xh * (gv * xh).mean(-1, keepdim=True)), size)
+    want = torch.zeros(H, dtype=torch.float64, device=DEV)
+    for b in range(0, T, 1 << 22):
+        want += (y[b: b + (1 << 22)].double() * (x[b: b + (1 << 22)].double() * rstd[b: b + (1 << 22)].double()[:, None])).sum(0)
+    # 512 workgroups add T/512 rows each in fp32, one after the other: T/512 * 2^-24 of a positive sum at most
+    _close(dw, want, want, extra=T / 512 * 2.0**-24)
+
+
 # ---- refusals (no GPU needed) ----
 
 @pytest.mark.parametrize("kw,status", [
