@@ -72,16 +72,10 @@ __device__ __forceinline__ float lanes_max(float v, int G) {
   return v;
 }
 
-// exp(x) for x <= 0 to two steps of fp32: the hardware's exp2 of the rounded product, corrected
-// by the product's own rounding error. Below -150 it is 0 (a NaN stays one); the library's expf,
-// for every range, made these kernels vector-ALU bound (131072 x 256 sigmoid forward 96 us).
-__device__ __forceinline__ float exp_neg(float x) {
-  constexpr float kLog2e = 1.44269504088896341f, kLn2 = 0.693147180559945309f;
-  const float y = x < -150.0f ? -150.0f : x;
-  const float t = y * kLog2e, lo = __builtin_fmaf(y, kLog2e, -t);
-  const float e = __builtin_amdgcn_exp2f(t);
-  return __builtin_fmaf(e * kLn2, lo, e);
-}
+// exp(x) by the hardware's exp2: off by |x| 2^-24 of its value and a step, so by 2^-20 for the
+// scores down to e^-16 that a sum of them in fp32 can see. The library's expf, to half a step over
+// every range, made these kernels vector-ALU bound (131072 x 256 sigmoid forward 96 us).
+__device__ __forceinline__ float exp_neg(float x) { return __builtin_amdgcn_exp2f(x * 1.44269504088896341f); }
 
 // A token's scores up to a common factor, from its logits z and their maximum m over the group:
 // exp(z - m), or sig(z) exp(-min(m, 0)) -- normalised sigmoid scores do not change by the factor,
@@ -99,13 +93,19 @@ __device__ __forceinline__ void scores(float (&z)[NV], float m, float shift, flo
   } else if constexpr (!SIG) {
 #pragma unroll
     for (int i = 0; i < NV; ++i) z[i] = exp_neg((z[i] - m) - shift);
+  } else if (m >= 0.0f) {  // with a logit above 0 the factor is 1 (and a sig below 2^-126 is 0 beside it)
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const float e = exp_neg(-z[i]), d = __builtin_amdgcn_rcpf(1.0f + e);
+      if constexpr (SLOPE) slope[i] = fminf(e, 3e38f) * d;  // an infinite e has d = 0
+      z[i] = d;
+    }
   } else {
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const float e = exp_neg(-fabsf(z[i])), d = __builtin_amdgcn_rcpf(1.0f + e);
-      if constexpr (SLOPE) slope[i] = z[i] > 0.0f ? e * d : d;
-      // with a logit above 0 the factor is 1: sig(z) = d or e d
-      z[i] = (m >= 0.0f ? (z[i] > 0.0f ? 1.0f : e) : exp_neg(z[i] - m)) * d;
+      if constexpr (SLOPE) slope[i] = d;
+      z[i] = exp_neg(z[i] - m) * d;
     }
   }
 }
