@@ -427,7 +427,8 @@ mok_status mok_norm_workspace_query(const mok_norm_desc* d, size_t* bwd_ws);
 /*
  * mok_rmsnorm_forward
  *   v = x + res (res may be NULL: v = x), in fp32;  rstd = 1 / sqrt(mean_h v^2 + eps);
- *   y = v * rstd * w;  each output is rounded once from fp32:
+ *   y = v * rstd * w;  each output is rounded once from fp32 (the squares are fp32 too: a row
+ *   whose sum of squares passes 3.4e38 has rstd = 0, one whose squares vanish rstd = eps^-1/2):
  *   r [T][H] (v: the residual stream for the next addition and the backward; may be NULL),
  *   y [T][H] (may be NULL when quant is MX), rstd [T] fp32 (may be NULL),
  *   q, s (quant MX, else NULL): y as stored in bf16, quantised in blocks of 32 along H as
@@ -452,7 +453,7 @@ mok_status mok_rmsnorm_backward(const mok_norm_desc* d, const void* dy, const vo
 
 /*
  * Balance loss of the router, per-expert counts, and the gradient by the router's logits.
- *   T tokens (0 <= T < 2^31), E experts (1..1024), k slots (1..min(E,16)).
+ *   T tokens (0 <= T < 2^31), E experts (1..1024), k slots (1..min(E,16)), T*k below 2^31.
  *   S: number of sequences (segments of consecutive tokens), 0..65535.  seg [S+1] int32 holds
  *   their offsets: segment s is tokens seg[s] .. seg[s+1]-1, 0 <= seg[0] <= ... <= seg[S] <= T
  *   (anything else gives unspecified results inside the arrays).  S = 0: one segment of all T
@@ -489,8 +490,8 @@ mok_status mok_balance_workspace_query(const mok_balance_desc* d, size_t* fwd_ws
  * Writes loss [2] fp32, counts [S][E] int32 (c), tokens [S+2] int32 (n_0.., then S' and N),
  * prob [S][E] fp32 (Pm; 0 where n_s = 0) and stat [T] fp32 (per counted token, for the
  * backward: log sum_f exp(z_tf - max_e z_te), or with MOK_SCORE_SIGMOID
- * exp(-min(max_e z_te, 0)) sum_f sig(z_tf); other tokens' are left as they were).  Sums over tokens are held in fp32 over the rows of a workgroup (at most
- * T/1024, or 256) and in fp64 beyond.
+ * exp(-min(max_e z_te, 0)) sum_f sig(z_tf); other tokens' are left as they were).  Sums over tokens
+ * are held in fp32 over the rows of a workgroup (at most T/1024, or 256) and in fp64 beyond.
  */
 mok_status mok_balance_forward(const mok_balance_desc* d, const float* logits, const int32_t* idx, const int32_t* seg,
                                const uint8_t* mask, float* loss, int32_t* counts, int32_t* tokens, float* prob,

@@ -29,6 +29,7 @@ mok_status check_balance(const mok_balance_desc* d) {
   if (d->reserved != 0) return MOK_ERR_SHAPE;
   if (d->T < 0 || d->T >= ((int64_t)1 << 31) || d->E < 1 || d->E > 1024) return MOK_ERR_SHAPE;
   if (d->k < 1 || d->k > 16 || d->k > d->E || d->S < 0 || d->S > 65535) return MOK_ERR_SHAPE;
+  if (d->T * d->k >= ((int64_t)1 << 31)) return MOK_ERR_SHAPE;  // an expert's count fits int32
   if (!std::isfinite(d->coef) || !std::isfinite(d->zcoef)) return MOK_ERR_SHAPE;
   if (d->zcoef != 0.0f && d->score != MOK_SCORE_SOFTMAX) return MOK_ERR_SHAPE;
   return MOK_OK;

@@ -384,7 +384,7 @@ __global__ __launch_bounds__(kThreadsB) void balance_grad_kernel(BalanceArgs a, 
   const int tid = threadIdx.x, g = tid / G, l = tid - g * G, groups = kThreadsB / G;
   const int64_t c0 = (int64_t)blockIdx.x * rows, c1 = min(a.T, c0 + rows);
   const int full = a.tokens[a.S], N = a.tokens[a.S + 1];
-  const float gz = N > 0 ? a.dloss[1] * a.zcoef * 2.0f / (float)N : 0.0f;
+  const float gz = N > 0 && a.zcoef != 0.0f ? a.dloss[1] * a.zcoef * 2.0f / (float)N : 0.0f;
   float zn[NV], stn = 0.0f;  // logits and stat of the next token, on their way
   uint8_t mn = 1;
   const auto fetch = [&](int64_t t) {
