@@ -96,6 +96,7 @@ LinearPlan linear_plan(int kind, int act, int epi, int64_t M, int N, int64_t K);
 size_t linear_part_bytes(int kind, int act, int epi, int64_t M, int N, int64_t K);
 hipError_t launch_linear(const LinearArgs& a, int kind, int act, int epi, bool out_f32, hipStream_t s);
 hipError_t launch_linear_bf16(const LinearArgs& a, int tile, int kind, int epi, bool out_f32, hipStream_t s);
+hipError_t launch_linear_f32(const LinearArgs& a, int tile, int kind, int epi, hipStream_t s);
 
 // dp = dy f'(pre) (epi != NONE; dp may be nullptr with NONE) and the column sums' parts
 // [linear_db_parts][P] fp32 (nullptr: not formed)

@@ -5,148 +5,6 @@ namespace mok {
 
 namespace {
 
-// K-contiguous operand rows with a ragged K: 16-byte chunks at or past K read as zeros.
-template <typename T, int ROWS>
-struct KTailStager {
-  static constexpr int VE = Elem<T>::VE;
-  static constexpr int BKE = kRowBytes / (int)sizeof(T);
-  static constexpr int NV = ROWS * 8 / kThreads;
-  const T* ptr[NV];
-  uint4 r[NV];
-  int64_t K;
-  int tid;
-  // rowptr(row): start of the row, or nullptr for a row of zeros
-  template <class F> __device__ __forceinline__ void init(int tid_, int64_t K_, F rowptr) {
-    tid = tid_;
-    K = K_;
-#pragma unroll
-    for (int v = 0; v < NV; ++v) ptr[v] = rowptr((tid + v * kThreads) >> 3);
-  }
-  __device__ __forceinline__ void load(int kt) {
-#pragma unroll
-    for (int v = 0; v < NV; ++v) {
-      const int64_t k = (int64_t)kt * BKE + ((tid + v * kThreads) & 7) * VE;
-      r[v] = ptr[v] != nullptr && k < K ? ldg16(ptr[v] + k) : make_uint4(0, 0, 0, 0);
-    }
-  }
-  __device__ __forceinline__ void store(char* lds) const {
-#pragma unroll
-    for (int v = 0; v < NV; ++v) {
-      const int i = tid + v * kThreads;
-      *reinterpret_cast<uint4*>(lds + lds_off(i >> 3, i & 7)) = r[v];
-    }
-  }
-};
-
-// MN-contiguous operand: element (k, mn) at base[k * ld + mn], zeros outside.
-template <typename T>
-struct MnSource {
-  const T* base;
-  int64_t ld, K, MN, mn0;
-  __device__ __forceinline__ uint4 operator()(int64_t k, int mn) const {
-    return k < K && mn0 + mn < MN ? ldg16(base + k * ld + mn0 + mn) : make_uint4(0, 0, 0, 0);
-  }
-};
-
-// One tile per workgroup: operands staged through registers into a double-buffered LDS tile
-// (gemm.h). PART: the tile's sums over a slice of K, for linear_join_kernel.
-template <class Tile, typename T, int KIND, int EPI, typename TO, bool PART>
-__global__ __launch_bounds__(256) void linear_simple_kernel(LinearArgs a) {
-  constexpr int PATCH = Tile::NW * 32 * kPatchLd * 4;  // the epilogue's
-  __shared__ __align__(1024) char smem[Tile::LDS_BYTES > PATCH ? Tile::LDS_BYTES : PATCH];
-  constexpr bool SW = EPI == MOK_EPI_SWIGLU;
-  constexpr int BKE = kRowBytes / (int)sizeof(T);
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, wm = wave >> 1, wn = wave & 1;
-  constexpr int BN = SW ? Tile::BN / 2 : Tile::BN;  // outputs of a tile's columns
-  const int NT = (a.N + BN - 1) / BN, MT = (int)((a.M + Tile::BM - 1) / Tile::BM);
-  const int slice = blockIdx.x / (MT * NT), L = blockIdx.x - slice * (MT * NT);
-  const int64_t m0 = (int64_t)(L / NT) * Tile::BM;
-  const int n0 = (L % NT) * BN;
-  const int64_t tiles = (a.K + BKE - 1) / BKE, kt0 = tiles * slice / a.split, kt1 = tiles * (slice + 1) / a.split;
-  const int64_t k0 = kt0 * BKE, k1 = min(a.K, kt1 * BKE);  // this slice
-  const int KT = (int)(kt1 - kt0);
-  f32x16_t acc[Tile::FM][Tile::FN];
-  const T* A = (const T*)a.a + (KIND == LIN_DW ? k0 * a.M : k0);
-  const T* B = (const T*)a.b + (KIND == LIN_FWD ? k0 : k0 * a.N);
-  // first output column of tile column j (SWIGLU: 32-column blocks of gate and up in turn)
-  const auto col = [&](int j) { return SW ? n0 + (j / Tile::WTN) * (Tile::WTN / 2) + (j & 31) : n0 + j; };
-  if constexpr (KIND == LIN_FWD) {
-    KTailStager<T, Tile::BM> sa;
-    sa.init(tid, k1 - k0, [&](int r) { return m0 + r < a.M ? A + (m0 + r) * a.K : nullptr; });
-    KTailStager<T, Tile::BN> sb;
-    sb.init(tid, k1 - k0, [&](int j) -> const T* {
-      const int c = col(j);
-      if (c >= a.N) return nullptr;
-      return B + (int64_t)(SW && (j & 32) ? a.N + c : c) * a.K;
-    });
-    main_loop<T, Tile>(sa, sb, KT, smem, wm, wn, lane, acc);
-  } else if constexpr (KIND == LIN_DX) {
-    KTailStager<T, Tile::BM> sa;
-    sa.init(tid, k1 - k0, [&](int r) { return m0 + r < a.M ? A + (m0 + r) * a.K : nullptr; });
-    MNStager<T, Tile::BN, MnSource<T>> sb;
-    sb.tid = tid;
-    sb.src = MnSource<T>{B, a.N, k1 - k0, a.N, n0};
-    main_loop<T, Tile>(sa, sb, KT, smem, wm, wn, lane, acc);
-  } else {
-    MNStager<T, Tile::BM, MnSource<T>> sa;
-    sa.tid = tid;
-    sa.src = MnSource<T>{A, a.M, k1 - k0, a.M, m0};
-    MNStager<T, Tile::BN, MnSource<T>> sb;
-    sb.tid = tid;
-    sb.src = MnSource<T>{B, a.N, k1 - k0, a.N, n0};
-    main_loop<T, Tile>(sa, sb, KT, smem, wm, wn, lane, acc);
-  }
-  __syncthreads();
-  epilogue16<Tile, SW>(acc, smem, wave, wm, wn, lane,
-                       [&](int row, int j, const float (&g)[16], const float (&u)[16]) {
-    const int64_t m = m0 + row;
-    if (m >= a.M) return;
-    const int c = col(j), P = SW ? 2 * a.N : a.N;
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      if (c + 8 * h >= a.N) continue;
-      float g8[8], u8[8];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        g8[i] = g[8 * h + i];
-        u8[i] = SW ? u[8 * h + i] : 0.0f;
-      }
-      if constexpr (PART) {
-        float* p = a.part + ((int64_t)slice * a.M + m) * P + c + 8 * h;
-        store8(p, g8);
-        if constexpr (SW) store8(p + a.N, u8);
-        continue;
-      }
-      if constexpr (KIND == LIN_FWD) linear_bias8<EPI>(a, c + 8 * h, g8, u8);
-      linear_store8<KIND, EPI, TO, T>(a, m, c + 8 * h, g8, u8, linear_add8<TO>(a, m, c + 8 * h));
-    }
-  });
-}
-
-template <class Tile, int KIND, int EPI>
-void run_simple(const LinearArgs& a, hipStream_t s) {
-  constexpr bool SW = EPI == MOK_EPI_SWIGLU;
-  const int bn = SW ? Tile::BN / 2 : Tile::BN;
-  const dim3 grid((unsigned)((int64_t)((a.N + bn - 1) / bn) * ((a.M + Tile::BM - 1) / Tile::BM) * a.split));
-  if (a.split == 1) {
-    hipLaunchKernelGGL((linear_simple_kernel<Tile, float, KIND, EPI, float, false>), grid, dim3(256), 0, s, a);
-    return;
-  }
-  hipLaunchKernelGGL((linear_simple_kernel<Tile, float, KIND, SW ? MOK_EPI_SWIGLU : MOK_EPI_NONE, float, true>), grid,
-                     dim3(256), 0, s, a);
-  linear_join<KIND, EPI, float, float>(a, s);
-}
-
-template <class Tile>
-void run_f32(const LinearArgs& a, int kind, int epi, hipStream_t s) {
-  if (kind == LIN_DX) run_simple<Tile, LIN_DX, MOK_EPI_NONE>(a, s);
-  else if (kind == LIN_DW) run_simple<Tile, LIN_DW, MOK_EPI_NONE>(a, s);
-  else if (epi == MOK_EPI_NONE) run_simple<Tile, LIN_FWD, MOK_EPI_NONE>(a, s);
-  else if (epi == MOK_EPI_SILU) run_simple<Tile, LIN_FWD, MOK_EPI_SILU>(a, s);
-  else if (epi == MOK_EPI_GELU) run_simple<Tile, LIN_FWD, MOK_EPI_GELU>(a, s);
-  else if constexpr (Tile::FN % 2 == 0) run_simple<Tile, LIN_FWD, MOK_EPI_SWIGLU>(a, s);  // gate and up side by side
-}
-
 // ---- dp = dy f'(pre), and the parts of the bias gradient ----
 // A thread keeps eight columns of dp and walks down the rows of its part; each input is read
 // once and dp written once (HBM-bound).
@@ -218,12 +76,12 @@ void run_dpre(const void* dy, const void* pre, int64_t M, int N, int epi, void* 
 
 }  // namespace
 
-// The plan of least estimated time. A tile's time is its K-tiles times what one takes (half as long
-// on an empty chip as on a full one), plus a fixed part (first loads, epilogue); the tiles go out in
-// rounds of as many as fit the 256 CUs. Slices of K cost their fp32 partial products' way to memory
-// and back, and a second launch. The constants (us) are fitted
-// to 28 shapes from 1 to 16384 rows at every tile and split: the plan taken is the fastest or within
-// a tenth of it.
+// The plan of least estimated time, with constants (us) fitted to 28 (bf16) and 17 (fp32) shapes
+// from 1 to 16384 rows at every tile and split: the plan taken is the fastest or within a tenth of it.
+// bf16: a tile's time is its K-tiles times what one takes (half as long on an empty chip as on a full
+// one), plus a fixed part (first loads, epilogue); the tiles go out in rounds of as many as fit the
+// 256 CUs. fp32, bound by its MFMAs: the K-tiles of the CU with the most tiles one after the other.
+// Slices of K cost their fp32 partial products' way to memory and back, and a second launch.
 LinearPlan linear_plan(int kind, int act, int epi, int64_t M, int N, int64_t K) {
   LinearPlan best{0, 1};
   if (M == 0) return best;
@@ -232,9 +90,9 @@ LinearPlan linear_plan(int kind, int act, int epi, int64_t M, int N, int64_t K) 
     double ktile, fixed;
   };
   static const Tile kTiles[4] = {
-      {256, 256, 1, 1.55, 11.0}, {128, 128, 2, 1.1, 5.0}, {64, 128, 3, 1.1, 4.0}, {32, 128, 4, 1.2, 3.5}};
-  static const Tile kTilesF32[2] = {{128, 128, 2, 4.6, 6.0}, {64, 64, 4, 2.9, 5.0}};  // K-tiles of 32
-  static const Tile kTilesF32Sw[2] = {{128, 128, 2, 4.6, 6.0}, {64, 128, 3, 3.6, 5.0}};
+      {256, 256, 1, 1.55, 11.0}, {128, 128, 2, 0.97, 5.0}, {64, 128, 3, 1.1, 4.0}, {32, 128, 4, 1.2, 3.5}};
+  static const Tile kTilesF32[2] = {{128, 128, 2, 1.75, 11.0}, {64, 64, 4, 0.45, 6.0}};  // K-tiles of 32
+  static const Tile kTilesF32Sw[2] = {{128, 128, 2, 1.75, 11.0}, {64, 128, 3, 1.05, 6.0}};
   const bool f32 = act == MOK_F32;
   const int64_t P = epi == MOK_EPI_SWIGLU ? 2 * (int64_t)N : N, kt = f32 ? (K + 31) / 32 : (K + 63) / 64;
   double least = 1e30;
@@ -244,10 +102,17 @@ LinearPlan linear_plan(int kind, int act, int epi, int64_t M, int N, int64_t K) 
     if (t > 0 && tiles >= (1 << 23)) continue;  // 2^32 threads a launch; the largest tile always fits
     for (int split = 1; split <= 256; split *= 2) {
       if (split > 1 && (kt / split < 2 || tiles * split >= (1 << 16))) break;
-      const double rounds = (double)((tiles * split + slots - 1) / slots);
-      const double fill = std::min(1.0, (double)(tiles * split) / (double)slots);
-      double us = rounds * ((double)((kt + split - 1) / split) * c.ktile * (0.5 + 0.5 * fill) + c.fixed);
-      if (split > 1) us += 5.0 + 8.0 * split * (double)M * (double)P / 4e6;
+      const double rounds = (double)((tiles * split + slots - 1) / slots), kts = (double)((kt + split - 1) / split);
+      const double bytes = 8.0 * split * (double)M * (double)P;  // of the partial products, written and read
+      double us;
+      if (f32) {
+        us = (double)((tiles * split + 255) / 256) * kts * c.ktile + c.fixed + 2.5 * rounds;
+        if (split > 1) us += 3.0 + bytes / 8e6;
+      } else {
+        const double fill = std::min(1.0, (double)(tiles * split) / (double)slots);
+        us = rounds * (kts * c.ktile * (0.5 + 0.5 * fill) + c.fixed);
+        if (split > 1) us += 5.0 + bytes / 4e6;
+      }
       if (us < least) {
         least = us;
         best = {t, split};
@@ -267,10 +132,7 @@ hipError_t launch_linear(const LinearArgs& args, int kind, int act, int epi, boo
   const LinearPlan p = linear_plan(kind, act, epi, a.M, a.N, a.K);
   a.split = p.split;
   if (act == MOK_BF16) return launch_linear_bf16(a, p.tile, kind, epi, out_f32, s);
-  if (p.tile == 0) run_f32<Tiling<128, 128, 2, 2>>(a, kind, epi, s);
-  else if (epi == MOK_EPI_SWIGLU) run_simple<Tiling<64, 128, 2, 2>, LIN_FWD, MOK_EPI_SWIGLU>(a, s);
-  else run_f32<Tiling<64, 64, 2, 2>>(a, kind, epi, s);
-  return hipGetLastError();
+  return launch_linear_f32(a, p.tile, kind, epi, s);
 }
 
 int linear_db_parts(int64_t M, int N) {
