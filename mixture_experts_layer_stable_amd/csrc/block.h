@@ -89,13 +89,15 @@ struct LinearArgs {
 };
 // Tile and slices of K of a product: a function of the shape and type only, so that the sums are.
 struct LinearPlan {
-  int tile;   // 0..3: 256x256, 128x128, 64x128, 32x128 (bf16); 0, 1: 128x128, 64x64 (SWIGLU 64x128) (fp32)
+  int tile;   // 0..3: 256x256, 128x128, 64x128, 32x128 (bf16); 0, 1: 128x128, 64x64 (SWIGLU 64x128) (fp32); kFewTile
   int split;
 };
+constexpr int kFewTile = 4;  // linear_few.hip
 LinearPlan linear_plan(int kind, int act, int epi, int64_t M, int N, int64_t K);
 size_t linear_part_bytes(int kind, int act, int epi, int64_t M, int N, int64_t K);
 hipError_t launch_linear(const LinearArgs& a, int kind, int act, int epi, bool out_f32, hipStream_t s);
 hipError_t launch_linear_bf16(const LinearArgs& a, int tile, int kind, int epi, bool out_f32, hipStream_t s);
+hipError_t launch_linear_few(const LinearArgs& a, int act, int epi, hipStream_t s);
 hipError_t launch_linear_f32(const LinearArgs& a, int tile, int kind, int epi, hipStream_t s);
 
 // dp = dy f'(pre) (epi != NONE; dp may be nullptr with NONE) and the column sums' parts

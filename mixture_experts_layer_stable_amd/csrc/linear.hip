@@ -119,6 +119,16 @@ LinearPlan linear_plan(int kind, int act, int epi, int64_t M, int N, int64_t K) 
       }
     }
   }
+  // Up to 32 rows, forward: linear_few.hip's kernel takes a round of eight 256-byte pieces of K at a
+  // time, `lat` us of latency each, or `full` when every CU has one of its workgroups; the tiles at
+  // least the time of their operands' way from HBM.
+  if (kind == LIN_FWD && M <= 32) {
+    const double lat = M <= 16 ? (f32 ? 1.1 : 0.7) : (f32 ? 1.6 : 1.15);
+    const double full = M <= 16 ? (f32 ? 1.6 : 1.35) : (f32 ? 2.5 : 2.0);
+    const int64_t es = f32 ? 4 : 2, piece = 8 * (256 / es), rounds = (K + piece - 1) / piece;
+    const double few = 4.0 + (double)rounds * std::max(lat, full * (double)((P + 15) / 16) / 256.0);
+    if (few < std::max(least, (double)(es * P * K) / 5.4e6)) best = {kFewTile, 1};
+  }
   return best;
 }
 
@@ -131,6 +141,7 @@ hipError_t launch_linear(const LinearArgs& args, int kind, int act, int epi, boo
   LinearArgs a = args;
   const LinearPlan p = linear_plan(kind, act, epi, a.M, a.N, a.K);
   a.split = p.split;
+  if (p.tile == kFewTile) return launch_linear_few(a, act, epi, s);
   if (act == MOK_BF16) return launch_linear_bf16(a, p.tile, kind, epi, out_f32, s);
   return launch_linear_f32(a, p.tile, kind, epi, s);
 }

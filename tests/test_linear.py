@@ -170,6 +170,19 @@ def test_larger_bf16(M, N, K):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("act", ["bf16", "f32"])
+@pytest.mark.parametrize("M,N,K", [(1, 8, 8), (1, 24, 1000), (2, 4104, 2056), (5, 2056, 4104), (15, 40, 72), (16, 1000, 520),
+                                   (17, 8, 2048), (31, 264, 1032), (32, 1032, 136), (33, 520, 264), (1, 16, 40000)])
+def test_few_rows(M, N, K, act):
+    """Single tokens and small batches of them; K shorter and longer than a round of pieces, odd ends."""
+    for epi in ("none", "silu", "gelu", "swiglu"):
+        print("case linear few", M, N, K, act, epi, flush=True)
+        c = Case(M, N, K, act, epi)
+        c.check_forward()
+        c.check_forward(bias=False, res=False)
+
+
+@pytest.mark.gpu
 def test_fp32_weight_gradients():
     for M, N, K in ((40, 24, 136), (1030, 384, 256)):
         c = Case(M, N, K, "bf16", "none", wgrad_f32=True)
