@@ -142,17 +142,11 @@ __device__ __forceinline__ int seg_of_wave(const BalanceArgs& a, int64_t t) {
   return lo;
 }
 
-// The loss from the sums over threads of l, its segments' parts, and z, lse^2, and from the
-// segments' tokens.
+// The loss from the sums over threads of l, its segments' parts, of z, lse^2, of n, counted tokens,
+// and of full, segments with some.
 template <int NT>
-__device__ void finish_loss(const BalanceArgs& a, double l, double z) {
+__device__ void finish_loss(const BalanceArgs& a, double l, double z, double n, double full) {
   __shared__ double s_w[NT / 64][4];
-  double n = 0.0, full = 0.0;
-  for (int i = threadIdx.x; i < a.S; i += NT) {
-    const int t = __hip_atomic_load(a.tokens + i, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    n += t;
-    full += t > 0;
-  }
   for (int o = 1; o < 64; o <<= 1) {
     l += __shfl_xor(l, o);
     z += __shfl_xor(z, o);
@@ -193,7 +187,7 @@ __global__ __launch_bounds__(NT) void balance_rows_kernel(BalanceArgs a, int G) 
   const int tid = threadIdx.x, g = tid / G, l = tid - g * G, groups = NT / G;
   const int64_t c0 = ALL ? 0 : (int64_t)blockIdx.x * a.rows, c1 = ALL ? a.T : min(a.T, c0 + a.rows);
   float zsum = 0.0f;
-  double loss = 0.0;
+  double loss = 0.0, all_n = 0.0, all_full = 0.0;
   if (!ALL && blockIdx.x == 0 && tid == 0) *a.done = 0;
   // The token that this group has on its way and its logits: loaded before anything is known of
   // segments and mask (a token that does not count is dropped later), so that one latency covers
@@ -295,13 +289,18 @@ __global__ __launch_bounds__(NT) void balance_rows_kernel(BalanceArgs a, int G) 
       }
     }
     if (tid == 0) {
-      if constexpr (ALL) a.tokens[s] = ns;
-      else a.wn[(int64_t)blockIdx.x + s] = ns;
+      if constexpr (ALL) {
+        a.tokens[s] = ns;
+        all_n += ns;
+        all_full += ns > 0;
+      } else {
+        a.wn[(int64_t)blockIdx.x + s] = ns;
+      }
     }
     __syncthreads();
   }
   if constexpr (ALL) {
-    finish_loss<NT>(a, loss, zsum);
+    finish_loss<NT>(a, loss, zsum, all_n, all_full);
   } else {
     zsum = lanes_sum(zsum, 64);
     if ((tid & 63) == 0) s_z[tid >> 6] = zsum;
@@ -371,11 +370,16 @@ __global__ __launch_bounds__(NT) void balance_seg_kernel(BalanceArgs a) {
   }
   __syncthreads();
   if (!s_last) return;
-  double l = 0.0, z = 0.0;
+  double l = 0.0, z = 0.0, nn = 0.0, full = 0.0;
   for (int i = tid; i < (int)(gridDim.x * gridDim.y); i += NT)
     l += __hip_atomic_load(a.wl + i, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
   for (int i = tid; i < a.chunks; i += NT) z += (double)a.wz[i];
-  finish_loss<NT>(a, l, z);
+  for (int i = tid; i < a.S; i += NT) {
+    const int t = __hip_atomic_load(a.tokens + i, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    nn += t;
+    full += t > 0;
+  }
+  finish_loss<NT>(a, l, z, nn, full);
 }
 
 template <typename TO, bool SIG, int VEC, int J>

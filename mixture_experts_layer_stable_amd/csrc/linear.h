@@ -46,6 +46,10 @@ __device__ __forceinline__ float sigmoid_f(float z) { return 1.0f / (1.0f + expf
 __device__ __forceinline__ float sigmoid_fast(float z) {
   return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(z * -1.44269504088896341f));
 }
+template <typename T>
+__device__ __forceinline__ float sigmoid_t(float z) {
+  return std::is_same<T, bf16>::value ? sigmoid_fast(z) : sigmoid_f(z);
+}
 __device__ __forceinline__ float phi_f(float z) { return 0.5f * erfcf(z * -0.70710678118654752f); }
 
 // What is added to columns c .. c+7 of row m, as it lies in memory (zeros without an addend).
@@ -81,8 +85,7 @@ __device__ __forceinline__ void linear_store8(const LinearArgs& a, int64_t m, in
     }
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      if constexpr (EPI == MOK_EPI_SILU || EPI == MOK_EPI_SWIGLU)
-        g[i] *= std::is_same<T, bf16>::value ? sigmoid_fast(g[i]) : sigmoid_f(g[i]);
+      if constexpr (EPI == MOK_EPI_SILU || EPI == MOK_EPI_SWIGLU) g[i] *= sigmoid_t<T>(g[i]);
       if constexpr (EPI == MOK_EPI_SWIGLU) g[i] *= u[i];
       if constexpr (EPI == MOK_EPI_GELU) g[i] *= phi_f(g[i]);
     }

@@ -8,7 +8,6 @@ namespace {
 // ---- dp = dy f'(pre), and the parts of the bias gradient ----
 // A thread keeps eight columns of dp and walks down the rows of its part; each input is read
 // once and dp written once (HBM-bound).
-constexpr int kDpreRows = 16;  // rows of a part, at least: its fp32 sums then stay an eighth of what is read
 
 template <typename T, int EPI>
 __global__ __launch_bounds__(256) void linear_dpre_kernel(const T* __restrict__ dy, const T* __restrict__ pre,
@@ -30,7 +29,7 @@ __global__ __launch_bounds__(256) void linear_dpre_kernel(const T* __restrict__ 
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       if constexpr (EPI == MOK_EPI_SILU || SW) {
-        const float s = sigmoid_f(p[i]), f = s * (1.0f + p[i] * (1.0f - s));
+        const float s = sigmoid_t<T>(p[i]), f = s * (1.0f + p[i] * (1.0f - s));
         if constexpr (SW) {
           const float up = d[i] * p[i] * s;
           d[i] *= u[i] * f;
@@ -53,15 +52,19 @@ __global__ __launch_bounds__(256) void linear_dpre_kernel(const T* __restrict__ 
   if constexpr (SW) store8(o + N, su);
 }
 
-// Rows of a part: the M rows go to about 2048 workgroups' worth of (256 x 8 columns, part).
-int64_t dpre_rows(int64_t M, int N) {
+// Rows of a part: the M rows go to about 2048 workgroups' worth of (256 x 8 columns, part). With sums
+// to write, a part has 16 rows, so that its fp32 sums stay an eighth of what is read, or as few as 4
+// where CUs would be left with fewer than two workgroups (2048 x (2 x 2048) with 16: 128 workgroups, 7 us
+// more than with 8; without sums, 8192 rows: 512 workgroups 41.7 us, 2048 28.4, 5.9 TB/s).
+int64_t dpre_rows(int64_t M, int N, bool sums) {
   const int64_t cols = (N + 2047) / 2048, parts = std::max<int64_t>(1, 2048 / cols);
-  return std::max<int64_t>(kDpreRows, (M + parts - 1) / parts);
+  const int64_t least = sums ? std::min<int64_t>(16, std::max<int64_t>(4, M * cols / 512)) : 1;
+  return std::max<int64_t>(least, (M + parts - 1) / parts);
 }
 
 template <typename T>
 void run_dpre(const void* dy, const void* pre, int64_t M, int N, int epi, void* dp, float* part, hipStream_t s) {
-  const int64_t rows = dpre_rows(M, N);
+  const int64_t rows = dpre_rows(M, N, part != nullptr);
   const dim3 grid((N + 2047) / 2048, (unsigned)((M + rows - 1) / rows)), block(256);
   const T *d = (const T*)dy, *p = (const T*)pre;
   if (epi == MOK_EPI_NONE)
@@ -148,7 +151,7 @@ hipError_t launch_linear(const LinearArgs& args, int kind, int act, int epi, boo
 
 int linear_db_parts(int64_t M, int N) {
   if (M == 0) return 0;
-  const int64_t rows = dpre_rows(M, N);
+  const int64_t rows = dpre_rows(M, N, true);
   return (int)((M + rows - 1) / rows);
 }
 
