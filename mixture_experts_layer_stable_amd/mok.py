@@ -362,6 +362,13 @@ def _ptr(name: str, t, dtype, shape, dev: int, optional=False):
                         t.device))
 
 
+def _dev(name: str, t) -> int:
+    """GPU of a required tensor, on which the call runs."""
+    if t is None:
+        raise ValueError("%s is required" % name)
+    return t.get_device()
+
+
 def _ws(t, dev: int):
     """(pointer, bytes) of a workspace tensor."""
     if t is None:
@@ -415,7 +422,7 @@ def norm_workspace_query(d: NormDesc) -> dict:
 
 def rmsnorm_forward(d: NormDesc, x, w, y=None, res=None, r=None, q=None, s=None, rstd=None, stream=None):
     """r = x + res; y = r * rstd * w; q, s = the MX rows of y (q [T, H] or, MXFP4, [T, H/2] bytes, s [H/128, T, 4])."""
-    T, H, t, dev, u8 = d.T, d.H, TORCH_DTYPE.get(d.act), x.get_device(), torch.uint8
+    T, H, t, dev, u8 = d.T, d.H, TORCH_DTYPE.get(d.act), _dev("x", x), torch.uint8
     rows = (T, H)
     mx = d.quant in (MXFP8, MXFP4)
     if not mx and (q is not None or s is not None):
@@ -430,7 +437,7 @@ def rmsnorm_forward(d: NormDesc, x, w, y=None, res=None, r=None, q=None, s=None,
 
 def rmsnorm_backward(d: NormDesc, dy, r, w, rstd, dx, dw=None, dr=None, ws=None, stream=None):
     """dx = dr + rstd * (g - xh * mean(g * xh)), dw = sum dy * xh, with xh = r * rstd and g = dy * w."""
-    T, H, t, dev = d.T, d.H, TORCH_DTYPE.get(d.act), dy.get_device()
+    T, H, t, dev = d.T, d.H, TORCH_DTYPE.get(d.act), _dev("dy", dy)
     rows = (T, H)
     wt = torch.float32 if d.flags & FLAG_WGRAD_F32 else t
     wp, wn = _ws(ws, dev)
@@ -475,7 +482,7 @@ def _mask(t, T, dev):
 def balance_forward(d: BalanceDesc, logits, idx, loss, counts, tokens, prob, stat, ws, seg=None, mask=None, stream=None):
     """loss [2], counts [S, E], tokens [S + 2], prob [S, E] and stat [T] from the router's logits [T, E] and idx [T, k];
     seg: offsets [S + 1] of the sequences, mask: [T] uint8 or bool."""
-    T, E, S, dev, f32, i32 = d.T, d.E, max(d.S, 1), logits.get_device(), torch.float32, torch.int32
+    T, E, S, dev, f32, i32 = d.T, d.E, max(d.S, 1), _dev("logits", logits), torch.float32, torch.int32
     wp, wn = _ws(ws, dev)
     _run(_lib.mok_balance_forward, "mok_balance_forward", dev, stream, d._c, _ptr("logits", logits, f32, (T, E), dev),
          _ptr("idx", idx, i32, (T, d.k), dev), _ptr("seg", seg, i32, (S + 1,), dev) if d.S > 0 else None,
@@ -486,7 +493,7 @@ def balance_forward(d: BalanceDesc, logits, idx, loss, counts, tokens, prob, sta
 
 def balance_backward(d: BalanceDesc, logits, counts, tokens, stat, dloss, dlogits, seg=None, mask=None, stream=None):
     """dlogits [T, E] (fp32, or bf16 with grad = BF16) of dloss[0] * loss[0] + dloss[1] * loss[1]."""
-    T, E, S, dev, f32, i32 = d.T, d.E, max(d.S, 1), logits.get_device(), torch.float32, torch.int32
+    T, E, S, dev, f32, i32 = d.T, d.E, max(d.S, 1), _dev("logits", logits), torch.float32, torch.int32
     _run(_lib.mok_balance_backward, "mok_balance_backward", dev, stream, d._c, _ptr("logits", logits, f32, (T, E), dev),
          _ptr("seg", seg, i32, (S + 1,), dev) if d.S > 0 else None, _mask(mask, T, dev),
          _ptr("counts", counts, i32, (S, E), dev), _ptr("tokens", tokens, i32, (S + 2,), dev),
@@ -524,7 +531,7 @@ def linear_workspace_query(d: LinearDesc) -> dict:
 
 def linear_forward(d: LinearDesc, x, w, y, bias=None, res=None, pre=None, ws=None, stream=None):
     """pre = x w^T + bias; y = f(pre) + res."""
-    M, N, K, P, t, dev = d.M, d.N, d.K, d.P, TORCH_DTYPE.get(d.act), x.get_device()
+    M, N, K, P, t, dev = d.M, d.N, d.K, d.P, TORCH_DTYPE.get(d.act), _dev("x", x)
     wp, wn = _ws(ws, dev)
     _run(_lib.mok_linear_forward, "mok_linear_forward", dev, stream, d._c, _ptr("x", x, t, (M, K), dev),
          _ptr("w", w, t, (P, K), dev), _ptr("bias", bias, torch.float32, (P,), dev, True),
@@ -535,7 +542,7 @@ def linear_forward(d: LinearDesc, x, w, y, bias=None, res=None, pre=None, ws=Non
 def linear_backward(d: LinearDesc, dy, x, w, dx=None, dw=None, db=None, pre=None, dx_add=None, dw_add=None, ws=None,
                     stream=None):
     """dp = dy f'(pre); dx = dp w + dx_add, dw = dp^T x + dw_add, db = sum dp (each only when its tensor is given)."""
-    M, N, K, P, t, dev = d.M, d.N, d.K, d.P, TORCH_DTYPE.get(d.act), dy.get_device()
+    M, N, K, P, t, dev = d.M, d.N, d.K, d.P, TORCH_DTYPE.get(d.act), _dev("dy", dy)
     wt = torch.float32 if d.flags & FLAG_WGRAD_F32 else t
     if (dx_add is not None and dx is None) or (dw_add is not None and dw is None):
         raise ValueError("dx_add, dw_add: without the gradient that they are added to")

@@ -289,6 +289,6 @@ def test_binding_refusals():
     good = dict(logits=f(4, 8), idx=f(4, 2, dtype=i), loss=f(2), counts=f(2, 8, dtype=i), tokens=f(4, dtype=i),
                 prob=f(2, 8), stat=f(4), ws=f(1 << 16, dtype=torch.uint8), seg=f(3, dtype=i))
     for bad in (dict(idx=f(4, 2, dtype=torch.int64)), dict(seg=None), dict(seg=f(4, dtype=i)), dict(mask=f(4)),
-                dict(counts=f(8, dtype=i)), dict(logits=f(8, 4).t()), dict()):
+                dict(counts=f(8, dtype=i)), dict(logits=f(8, 4).t()), dict(logits=None), dict()):
         with pytest.raises(ValueError):
             mok.balance_forward(d, **{**good, **bad})

@@ -331,7 +331,7 @@ def test_binding_refusals():
     d = mok.LinearDesc(4, 16, 8)
     z = lambda *s: torch.zeros(*s, dtype=torch.bfloat16)
     good = dict(x=z(4, 8), w=z(16, 8), y=z(4, 16))
-    for bad in (dict(w=z(8, 16).t()), dict(x=z(4, 8).float()), dict(y=z(4, 8)), dict(bias=z(16)), dict(res=z(16, 4)), dict()):
+    for bad in (dict(w=z(8, 16).t()), dict(x=z(4, 8).float()), dict(y=z(4, 8)), dict(x=None), dict(bias=z(16)), dict(res=z(16, 4)), dict()):
         with pytest.raises(ValueError):
             mok.linear_forward(d, **{**good, **bad})
     with pytest.raises(ValueError):

@@ -338,7 +338,7 @@ def test_binding_refusals():
     t = torch.zeros(4, 128, dtype=torch.bfloat16)
     w = torch.ones(128, dtype=torch.bfloat16)
     for bad in (dict(x=t.float()), dict(x=t[:3]), dict(w=w[:64]), dict(y=torch.zeros(128, 4, dtype=torch.bfloat16).t()),
-                dict(res=t.half()), dict(q=torch.zeros(4, 128, dtype=torch.uint8)), dict(y=None), dict()):
+                dict(res=t.half()), dict(q=torch.zeros(4, 128, dtype=torch.uint8)), dict(y=None), dict(x=None), dict()):
         a = {**dict(x=t, w=w, y=t.clone()), **bad}
         with pytest.raises(ValueError):   # the last one: tensors that are not on the GPU
             mok.rmsnorm_forward(d, a.pop("x"), a.pop("w"), **a)
