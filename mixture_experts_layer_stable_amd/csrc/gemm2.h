@@ -35,9 +35,11 @@ extern __device__ uint4 g_zero_1k[64];
 // outstanding loads, vmcnt(0), before each LDS read and collapse the ring to
 // one stage). Completion is tracked explicitly with wait_vmcnt below; loads
 // complete in issue order, so compiler-managed waits on later loads stay valid.
+// A scalar write of M0 needs one wait state before a load into LDS reads it (the s_nop),
+// which the compiler keeps for its own loads but does not add inside inline asm.
 __device__ __forceinline__ void dma16(const void* src, char* lds_wave_base) {
   const uint32_t l = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(lds_void_t)lds_wave_base);
-  asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(l), "v"(src) : "memory", "m0");
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(l), "v"(src) : "memory", "m0");
 }
 
 // s_waitcnt with vmcnt <= N (N < 64), no wait on the other counters.
@@ -67,7 +69,8 @@ __device__ __forceinline__ const char* uniform_ptr(const char* p) {
 
 __device__ __forceinline__ void dma16_sv(const char* sbase, uint32_t voff, char* lds_wave_base) {
   const uint32_t l = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(lds_void_t)lds_wave_base);
-  asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(l), "v"(voff), "s"(sbase) : "memory", "m0");
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2"
+               ::"s"(l), "v"(voff), "s"(sbase) : "memory", "m0");
 }
 
 __device__ __forceinline__ uint4 tr_pair(const char* a0, const char* a1) {

@@ -18,7 +18,8 @@ __device__ __forceinline__ uint32_t lds_offset(const char* p) {
 }
 
 __device__ __forceinline__ void dma16_at(const char* sbase, uint32_t voff, uint32_t lds) {
-  asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(lds), "v"(voff), "s"(sbase) : "memory", "m0");
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2"
+               ::"s"(lds), "v"(voff), "s"(sbase) : "memory", "m0");
 }
 
 static __device__ uint4 g_zero_16 = {};  // what is read past the end of K
@@ -81,7 +82,8 @@ struct DenseK {
     }
   }
   __device__ __forceinline__ static void dma16_any(const char* p, uint32_t lds) {
-    asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(lds), "v"(p) : "memory", "m0");
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off"
+                 ::"s"(lds), "v"(p) : "memory", "m0");
   }
   __device__ __forceinline__ uint4 frag(const char* stage, int f, int ks) const {
     return *reinterpret_cast<const uint4*>(stage + foff[f][ks]);
