@@ -35,8 +35,10 @@ extern __device__ uint4 g_zero_1k[64];
 // outstanding loads, vmcnt(0), before each LDS read and collapse the ring to
 // one stage). Completion is tracked explicitly with wait_vmcnt below; loads
 // complete in issue order, so compiler-managed waits on later loads stay valid.
-// A scalar write of M0 needs one wait state before a load into LDS reads it (the s_nop),
-// which the compiler keeps for its own loads but does not add inside inline asm.
+// Two distances that the compiler keeps for its own loads but cannot see to inside inline
+// asm: one wait state from a scalar write of M0 to a load into LDS (the s_nop here, the
+// s_mov_b64 in load_lds_sv), and five from a vector instruction's write of an SGPR
+// (v_readfirstlane, v_readlane of a spilled one) to a load that takes its address from it.
 __device__ __forceinline__ void dma16(const void* src, char* lds_wave_base) {
   const uint32_t l = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(lds_void_t)lds_wave_base);
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(l), "v"(src) : "memory", "m0");
@@ -67,10 +69,24 @@ __device__ __forceinline__ const char* uniform_ptr(const char* p) {
   return reinterpret_cast<const char*>((uintptr_t)(((uint64_t)hi << 32) | lo));
 }
 
+// The load itself, 16 or 4 bytes a lane. Its base goes through a scalar move, which the
+// hardware holds back until a vector instruction's write of the source has arrived and
+// whose result a load may read at once.
+template <int BYTES>
+__device__ __forceinline__ void load_lds_sv(const char* sbase, uint32_t voff, uint32_t lds) {
+  static_assert(BYTES == 16 || BYTES == 4, "bytes per lane");
+  uint64_t base;
+  if constexpr (BYTES == 16)
+    asm volatile("s_mov_b32 m0, %1\n\ts_mov_b64 %0, %3\n\tglobal_load_lds_dwordx4 %2, %0"
+                 : "=&s"(base) : "s"(lds), "v"(voff), "s"(sbase) : "memory", "m0");
+  else
+    asm volatile("s_mov_b32 m0, %1\n\ts_mov_b64 %0, %3\n\tglobal_load_lds_dword %2, %0"
+                 : "=&s"(base) : "s"(lds), "v"(voff), "s"(sbase) : "memory", "m0");
+}
+
 __device__ __forceinline__ void dma16_sv(const char* sbase, uint32_t voff, char* lds_wave_base) {
-  const uint32_t l = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(lds_void_t)lds_wave_base);
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2"
-               ::"s"(l), "v"(voff), "s"(sbase) : "memory", "m0");
+  load_lds_sv<16>(sbase, voff,
+                  __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(lds_void_t)lds_wave_base));
 }
 
 __device__ __forceinline__ uint4 tr_pair(const char* a0, const char* a1) {

@@ -38,9 +38,8 @@ constexpr int kMxStages = 3;
 
 // One-dword-per-lane DMA: lane l's 4 bytes land at LDS base + 4*l.
 __device__ __forceinline__ void dma4_sv(const char* sbase, uint32_t voff, char* lds_wave_base) {
-  const uint32_t l = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(lds_void_t)lds_wave_base);
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, %2"
-               ::"s"(l), "v"(voff), "s"(sbase) : "memory", "m0");
+  load_lds_sv<4>(sbase, voff,
+                 __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(lds_void_t)lds_wave_base));
 }
 
 // Scale dwords of ROWS tile rows per K-tile: SD per row (one per 128 elements of the

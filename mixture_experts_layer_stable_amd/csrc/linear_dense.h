@@ -17,11 +17,6 @@ __device__ __forceinline__ uint32_t lds_offset(const char* p) {
   return __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(lds_void_t)p);
 }
 
-__device__ __forceinline__ void dma16_at(const char* sbase, uint32_t voff, uint32_t lds) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2"
-               ::"s"(lds), "v"(voff), "s"(sbase) : "memory", "m0");
-}
-
 static __device__ uint4 g_zero_16 = {};  // what is read past the end of K
 
 // K-contiguous operand: tile row r starts at sbase + voff(r); K-tile kt is its bytes
@@ -68,7 +63,8 @@ struct DenseK {
   __device__ __forceinline__ void issue(int64_t kt, uint32_t lds, int wave, int j0 = 0, int j1 = NI) const {
     if (FULL || (kt + 1) * 128 <= kbytes) {
 #pragma unroll
-      for (int j = j0; j < j1; ++j) dma16_at(uniform_ptr(base(kt, j, wave)), voff[j], lds + (wave + NW * j) * 1024);
+      for (int j = j0; j < j1; ++j)
+        load_lds_sv<16>(uniform_ptr(base(kt, j, wave)), voff[j], lds + (wave + NW * j) * 1024);
     } else {
       const int lane = threadIdx.x & 63;
 #pragma unroll
@@ -140,7 +136,7 @@ struct DenseMN {
     if (FULL || k0 + KR <= K) {
       const char* b = uniform_ptr(sbase + k0 * ld);
 #pragma unroll
-      for (int j = j0; j < j1; ++j) dma16_at(b, voff[j], lds + (wave + NW * j) * 1024);
+      for (int j = j0; j < j1; ++j) load_lds_sv<16>(b, voff[j], lds + (wave + NW * j) * 1024);
     } else {
 #pragma unroll
       for (int j = j0; j < j1; ++j) {
