@@ -308,7 +308,7 @@ def x_quant_views(d: Desc, fwd_ws):
     """The quantised x rows of micro-batch d.mb_index in the forward workspace: q [T, H] (MXFP4: [T, H/2]) and
     s [H/128, T, 4], where rmsnorm_forward writes them for a moe_forward with FLAG_X_QUANT."""
     L = mx_layout_query(d)
-    o = (d.mb_index % d.ring) * L["fwd_slot"]
+    o = (d.mb_index % max(d.ring, 1)) * L["fwd_slot"]
     hq = d.H // 2 if d.gemm == MXFP4 else d.H
     q = fwd_ws[o + L["xq"]: o + L["xq"] + d.T * hq].view(d.T, hq)
     return q, fwd_ws[o + L["xs"]: o + L["xs"] + d.T * d.H // 32].view(d.H // 128, d.T, 4)
