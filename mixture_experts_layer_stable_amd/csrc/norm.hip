@@ -36,11 +36,15 @@ __device__ __forceinline__ V group_sum(V v, int G, V* s_red) {
   return t;
 }
 
-// 1 / sqrt(x) to half a step: the hardware's estimate and one Newton step on its exact residual.
-__device__ __forceinline__ float rsqrt_round(float x) {
+// 1 / sqrt(x) to half a step: the hardware's estimate and one Newton step on its exact residual. The
+// estimate takes a subnormal x for 0: it is formed of x 2^24, which is exact, as is the factor 2^12 after.
+__device__ __forceinline__ float rsqrt_round(float mean) {
+  const bool tiny = mean < 0x1p-126f;
+  const float x = tiny ? mean * 0x1p24f : mean;
   const float r = __builtin_amdgcn_rsqf(x), h = x * r;
   const float e = __builtin_fmaf(-h, r, 1.0f) - __builtin_fmaf(x, r, -h) * r;  // 1 - x r^2
-  return x > 0.0f && x < INFINITY ? __builtin_fmaf(0.5f * r, e, r) : r;
+  const float y = x > 0.0f && x < INFINITY ? __builtin_fmaf(0.5f * r, e, r) : r;
+  return tiny ? y * 0x1p12f : y;
 }
 
 // Lanes per row, rows per workgroup and vectors per lane for rows of nv vectors: small rows
