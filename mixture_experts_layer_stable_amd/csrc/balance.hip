@@ -203,7 +203,10 @@ __global__ __launch_bounds__(NT) void balance_rows_kernel(BalanceArgs a, int G) 
     const int64_t s0 = seg_at(a, s), s1 = seg_at(a, s + 1);
     if (!ALL && s0 >= c1) break;
     const int64_t t0 = max(s0, c0), t1 = min(s1, c1);
-    if (!ALL && t1 <= t0) continue;
+    if (!ALL && t1 <= t0) {  // one of a run of empty segments, maybe: on with the one that holds token t0
+      s = max(s, seg_of_wave(a, t0) - 1);
+      continue;
+    }
     if (tn != t0 + g) fetch(t0 + g, t1);
     bool on = t0 + g < t1 && (a.mask == nullptr || a.mask[t0 + g] != 0);
     for (int e = tid; e < a.E; e += NT) s_c[e] = 0;

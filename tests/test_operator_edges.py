@@ -38,6 +38,45 @@ def test_norm_of_rows_with_subnormal_squares():
     assert (y[5] == 0).all()          # eps = 1e-39: a zero row stays one
 
 
+@pytest.mark.gpu
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("T,E,k,cuts", [
+    (4096, 8, 2, [0] + [1001] * 5000 + [4096]), (4096, 8, 2, [0, 256] + [300] * 4000 + [301] + [512] * 100 + [600] * 100 + [4096]),
+    (700, 384, 4, [5] * 70 + [33] * 200 + [34] * 64 + [698]), (40, 16, 2, [7] * 65 + [8] * 130 + [39] * 3 + [40] * 70),
+])
+def test_balance_with_runs_of_empty_sequences(T, E, k, cuts, score):
+    from test_balance import Run, check, inputs
+    print("case balance empties", T, E, len(cuts) - 1, score, flush=True)
+    z, idx, dl, g = inputs(T, E, k, T + E)
+    seg = torch.tensor(cuts, dtype=torch.int32, device=DEV)
+    mask = (torch.rand(T, generator=g) < 0.8).to(DEV)
+    soft = score == "softmax"
+    check(Run(T, E, k, len(cuts) - 1, score, "f32", zcoef=0.1 if soft else 0.0), z, idx, dl, seg, mask, soft)
+
+
+@pytest.mark.gpu
+def test_empty_sequences_cost_the_same_wherever_they_lie():
+    """60000 empty sequences in the middle of the tokens take no longer than behind the last token (which is what the
+    second launch takes for them); one after the other they would be 60000 dependent loads."""
+    from test_balance import Run, inputs
+    T, E, k, S = 4096, 8, 2, 60000
+    z, idx, dl, _ = inputs(T, E, k, 1)
+    us = {}
+    for name, cuts in (("behind", [0, 1001] + [T] * (S - 1)), ("inside", [0] + [1001] * (S - 1) + [T])):
+        seg = torch.tensor(cuts, dtype=torch.int32, device=DEV)
+        run, times = Run(T, E, k, S, "softmax", "f32"), []
+        for _ in range(6):
+            a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+            a.record()
+            run.mok.balance_forward(run.d, z, idx, run.loss, run.counts, run.tokens, run.prob, run.stat, run.ws, seg=seg)
+            b.record()
+            b.synchronize()
+            times.append(a.elapsed_time(b) * 1e3)
+        us[name] = sorted(times)[2]
+    print("60000 empty sequences, us:", us, flush=True)
+    assert us["inside"] < 3 * us["behind"], us
+
+
 def test_x_quant_views_of_a_ring_given_as_0():
     """mb_count and ring 0 stand for 1."""
     mok = _mok()
