@@ -278,12 +278,12 @@ __global__ __launch_bounds__(NT) void balance_rows_kernel(BalanceArgs a, int G) 
     __syncthreads();
     const int ns = s_n;
     for (int e = tid; e < a.E; e += NT) {
-      float v = 0.0f;
+      std::conditional_t<ALL, double, float> v = 0;  // ALL: the waves' sums are the partial rows
 #pragma unroll
       for (int i = 0; i < NW; ++i) v += s_q[i * a.E + e];
       if constexpr (ALL) {
         a.counts[(int64_t)s * a.E + e] = s_c[e];
-        a.prob[(int64_t)s * a.E + e] = ns > 0 ? v / (float)ns : 0.0f;
+        a.prob[(int64_t)s * a.E + e] = ns > 0 ? (float)(v / ns) : 0.0f;
         if (ns > 0) loss += (double)s_c[e] * v * ((double)a.E / ((double)a.k * ns * ns));
       } else {
         const int64_t at = (int64_t)blockIdx.x + s;

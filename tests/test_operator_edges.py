@@ -77,6 +77,39 @@ def test_empty_sequences_cost_the_same_wherever_they_lie():
     assert us["inside"] < 3 * us["behind"], us
 
 
+@pytest.mark.gpu
+@pytest.mark.parametrize("E", [1, 2, 3, 4])
+def test_a_small_batch_adds_its_waves_in_64_bits(E):
+    """T * E at the limit of one workgroup. The first of every 1024 tokens have p = 1 for expert 0 in the first wave and
+    0.4 of a step of that wave's sum, in all, in each other wave: added one after the other in fp32 they would be lost."""
+    from test_balance import Run
+    k = 1
+    T = (1 << 14) // E // 1024 * 1024
+    groups = 1024                       # tokens that the workgroup takes at once (one lane each)
+    own = T // groups * 64              # tokens of a wave
+    z = torch.zeros(T, E, device=DEV)
+    tok = torch.arange(T, device=DEV) % groups // 64
+    p = 1.0
+    if E > 1:
+        step = 2.0 ** (own.bit_length() - 1 - 23)
+        p = 0.4 * step / own
+        z[:, 0] = torch.where(tok == 0, 0.0, torch.log(torch.tensor(p * (E - 1), dtype=torch.float64)).float())
+        z[:, 1:] = torch.where(tok == 0, -float("inf"), 0.0)[:, None]
+    idx = torch.zeros(T, k, dtype=torch.int32, device=DEV)
+    run = Run(T, E, k, 0, "softmax", "f32", coef=0.5)
+    loss, counts, tokens, prob, _ = run(z, idx, torch.ones(2, device=DEV))
+    want = torch.softmax(z.double(), 1).mean(0)
+    # p to 2^-20 each (its share of the sum is 15 * 0.4 steps), a wave's sum of equal values within 2^-24 for each of its
+    # T / 1024 + 6 additions (of ones: exact); the mean's own rounding
+    small = own * 15 * p if E > 1 else 0.0
+    tol = 2.0**-24 * want[0] + (2.0**-20 + (T // groups + 6) * 2.0**-24) * small / T
+    print("small batch", E, T, float((prob[0, 0].double() - want[0]) / (2.0**-24 * want[0])), flush=True)
+    assert (prob[0, 0].double() - want[0]).abs() <= tol * 1.01
+    l0 = run.d.coef * E * want[0]       # every slot is expert 0's
+    assert (loss[0].double() - l0).abs() <= (tol / want[0] + 2.0**-24) * l0
+    assert int(counts[0, 0]) == T and tokens.tolist() == [T, 1, T]
+
+
 def test_x_quant_views_of_a_ring_given_as_0():
     """mb_count and ring 0 stand for 1."""
     mok = _mok()
