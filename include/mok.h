@@ -492,7 +492,7 @@ mok_status mok_balance_workspace_query(const mok_balance_desc* d, size_t* fwd_ws
  * backward: log sum_f exp(z_tf - max_e z_te), or with MOK_SCORE_SIGMOID
  * exp(-min(max_e z_te, 0)) sum_f sig(z_tf); other tokens' are left as they were).  Sums over tokens
  * are held in fp32 over the rows of a workgroup (at most T/1024, or 256) and in fp64 beyond; one
- * workgroup alone (T*E up to 2^14, S up to 64) holds them in fp32 over the rows of a wave, a sixteenth.
+ * workgroup alone (T*E up to 2^14, S up to 4) holds them in fp32 over the rows of a wave, a sixteenth.
  */
 mok_status mok_balance_forward(const mok_balance_desc* d, const float* logits, const int32_t* idx, const int32_t* seg,
                                const uint8_t* mask, float* loss, int32_t* counts, int32_t* tokens, float* prob,

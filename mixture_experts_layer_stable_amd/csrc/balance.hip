@@ -23,8 +23,13 @@ constexpr int kThreadsB = 256;
 // Four workgroups per CU, as long as a chunk keeps 16 rows (T = 16384, E = 384, 37 segments: 64 rows
 // 51.8 us, 32 rows 46, 16 rows 43.9) and one for each group of lanes.
 constexpr int kBalanceChunks = 1024, kBalanceRows = 16;
-constexpr int64_t kBalanceSmall = 1 << 14;  // logits of a batch for one workgroup
-constexpr int kBalanceSmallSegs = 64;
+// One workgroup for the whole batch: up to 2^14 logits of one segment (E = 8, us against two launches: 64
+// tokens 9.6, 11.5; 2048 tokens 11.7, 12.5). It walks its segments one after the other, 3 to 6 us each, as
+// does the workgroup of each chunk: a batch of one chunk gains the launch up to four of them (64 tokens, E = 8, 4
+// segments: 23.9, 26.0; 16: 81, 79), a batch of more chunks nothing (2048 tokens, E = 8, 2 segments: 16.1,
+// 13.5; 256 tokens, E = 64, 64 segments: 415, 103).
+constexpr int64_t kBalanceSmall = 1 << 14;
+constexpr int kBalanceSmallSegs = 4;
 constexpr int kSegExperts = 16;  // of a workgroup of the second launch, at least
 
 // Logits of one token over G lanes: J vectors of VEC per lane (vector j*G + lane), at most 16
@@ -518,7 +523,7 @@ BalanceWs balance_ws(int64_t T, int E, int S) {
 
 hipError_t launch_balance_fwd(const BalanceArgs& a, hipStream_t s) {
   const RowShape r = row_shape(a.E);
-  const bool all = a.T * a.E <= kBalanceSmall && a.S <= kBalanceSmallSegs;
+  const bool all = a.T * a.E <= kBalanceSmall && a.S <= (a.chunks == 1 ? kBalanceSmallSegs : 1);
   with_shape(r, [&](auto v, auto j) {
     constexpr int V = decltype(v)::value, JJ = decltype(j)::value;
     const auto go = [&](auto sig) {

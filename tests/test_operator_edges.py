@@ -78,6 +78,30 @@ def test_empty_sequences_cost_the_same_wherever_they_lie():
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("T,E", [(2048, 8), (256, 64)])
+def test_small_batches_of_many_sequences_take_the_faster_path(T, E):
+    """64 sequences in one workgroup would take two to four times as long as 65, which are too many for it."""
+    from test_balance import Run, inputs
+    us = {}
+    for S in (64, 65):
+        z, idx, _, _ = inputs(T, E, 2, 1)
+        seg = torch.linspace(0, T, 65).int().tolist() + [T] * (S - 64)
+        run, times = Run(T, E, 2, S, "softmax", "f32"), []
+        seg = torch.tensor(seg, dtype=torch.int32, device=DEV)
+        for _ in range(11):
+            a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+            a.record()
+            for _ in range(10):
+                run.mok.balance_forward(run.d, z, idx, run.loss, run.counts, run.tokens, run.prob, run.stat, run.ws, seg=seg)
+            b.record()
+            b.synchronize()
+            times.append(a.elapsed_time(b) * 100)
+        us[S] = sorted(times)[5]
+    print("sequences, us:", us, flush=True)
+    assert us[64] < 1.4 * us[65], us
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("E", [1, 2, 3, 4])
 def test_a_small_batch_adds_its_waves_in_64_bits(E):
     """T * E at the limit of one workgroup. The first of every 1024 tokens have p = 1 for expert 0 in the first wave and
