@@ -432,7 +432,8 @@ mok_status mok_norm_workspace_query(const mok_norm_desc* d, size_t* bwd_ws);
  *   r [T][H] (v: the residual stream for the next addition and the backward; may be NULL),
  *   y [T][H] (may be NULL when quant is MX), rstd [T] fp32 (may be NULL),
  *   q, s (quant MX, else NULL): y as stored in bf16, quantised in blocks of 32 along H as
- *   the layer quantises x: q [T][H] E4M3 bytes or [T][H/2] E2M1 pairs, s [H/128][T][4].
+ *   the layer quantises x: q [T][H] E4M3 bytes or [T][H/2] E2M1 pairs, s [H/128][T][4] (of
+ *   finite y: a block with a NaN or an infinity has no MX form and gets finite elements).
  * r and y may each be the same array as x or as res (not the same as each other); other
  * overlaps are not allowed.
  */
@@ -445,7 +446,8 @@ mok_status mok_rmsnorm_forward(const mok_norm_desc* d, const void* x, const void
  *   dw_h = sum_t dy * xh.
  * r [T][H] and rstd [T] as the forward wrote them (r = x without a residual); dr may be NULL
  * (0).  dx [T][H] may be the same array as dy or dr (not as r).  dw [H] in act (fp32 with
- * MOK_FLAG_WGRAD_F32) may be NULL; every element is written (zero for T = 0).  ws is used
+ * MOK_FLAG_WGRAD_F32) may be NULL; every element is written (zero for T = 0).  Its sums are
+ * held in fp32: up to 512 parts of at most T/512 rows one after the other.  ws is used
  * (and required) only with dw.
  */
 mok_status mok_rmsnorm_backward(const mok_norm_desc* d, const void* dy, const void* dr, const void* r, const void* w,

@@ -5,10 +5,12 @@
 // holds one token's logits in registers (one read, the next token's on their way), forms its
 // scores and adds them to the lanes' own per-expert sums; slots are counted with integer LDS
 // atomics; where a segment ends inside the chunk the sums are written out as the partial row of
-// (chunk, segment). (2) one workgroup per (64 experts, segment) adds the segment's partial rows;
-// the last of them adds the parts of the loss. Batches of up to 2^14 logits take one launch of one
-// workgroup for all of it. No float atomics: the sums depend on T, E and the segments only. Bound
-// by HBM (logits read once) or, for small batches, by the launches.
+// (chunk, segment). (2) one workgroup per (64 experts, segment), or per 16 where a segment has many
+// partial rows, adds the segment's partial rows; the last of them, by a count on one word (13 ns a
+// workgroup: 60000 segments take 0.8 ms), adds the parts of the loss. Small batches take one launch
+// of one workgroup for all of it (kBalanceSmall). No float atomics: the sums depend on T, E and the
+// segments only. Bound by its loads (131072 x 256: 45 us, 3.1 TB/s, and 11 for the 16 workgroups of the
+// second launch); for small batches by the launches, for short segments by the walk over a chunk's.
 // Backward: one launch, one read of the logits and one write of their gradient.
 #include <cmath>
 

@@ -60,7 +60,7 @@ struct BalanceArgs {
   int32_t* wn;         // [chunks + S] tokens
   float* wz;           // [chunks] sums of lse^2
   int32_t* done;       // workgroups of the second launch that are through
-  double* wl;          // [S][ceil(E / 64)] parts of the loss
+  double* wl;          // [S][workgroups of a segment in the second launch] parts of the loss
   const float* dloss;
   void* dlogits;
 };

@@ -28,7 +28,7 @@ __device__ __forceinline__ uint32_t f32_to_bf16(float f) {
 
 // Two floats -> two bf16 packed in one dword (lo in bits 0..15), round to nearest
 // even, by the hardware conversion (v_cvt_pk_bf16_f32). For finite values and
-// infinities it gives the same bits as f32_to_bf16; NaN inputs do not occur here.
+// infinities it gives the same bits as f32_to_bf16; a NaN stays one.
 typedef __bf16 bf16x2_hw_t __attribute__((ext_vector_type(2)));
 typedef float f32x2_t __attribute__((ext_vector_type(2)));
 __device__ __forceinline__ uint32_t bf16x2_rne(float lo, float hi) {

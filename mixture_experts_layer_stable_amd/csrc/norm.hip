@@ -177,10 +177,11 @@ hipError_t launch_norm_fwd(const NormArgs& a, int act, int quant, hipStream_t s)
 }
 
 // Backward: a workgroup takes row groups blockIdx, blockIdx + grid, ... and keeps its columns'
-// share of dw in registers; the row groups of a workgroup are added in LDS in group order and
-// written as one partial row. dr is loaded with dy and r, ahead of the row's sum (16384 x 7168:
-// 202 -> 172 us, 5.5 TB/s; the next row's loads ahead of the sum too: 265, its registers spill);
-// 512 workgroups, two per CU (768: 205 us, 1024: 180, 256: 321).
+// share of dw in registers, in fp32, one row after the other (T / 512 of them; fewer where rows lie
+// side by side); the row groups of a workgroup are added in LDS in group order and written as one
+// partial row. dr is loaded with dy and r, ahead of the row's sum (16384 x 7168: 202 -> 172 us, 5.5
+// TB/s; the next row's loads ahead of the sum too: 265, its registers spill); 512 workgroups, two per
+// CU (768: 205 us, 1024: 180, 256: 321).
 template <typename T, int VPT, bool NT>
 __global__ __launch_bounds__(1024) void norm_bwd_kernel(NormArgs a, int G) {
   constexpr int VE = Elem<T>::VE;
