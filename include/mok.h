@@ -366,7 +366,7 @@ mok_status mok_moe_backward(const mok_desc* d, void* sched, const void* x, const
  * "fc1", "fc2", "combine", "dh", "router_bwd", "dx", "dx_reduce", "gather",
  * "dw2", "dw1", "dwr", for MXFP8 "quant" (row quantisers and stash
  * copies), "flush" (block table and token-axis quantisers), and the operators around the
- * layer, "norm", "balance", "linear", or "*" for all --
+ * layer, "norm", "balance", "linear", "grouped", "q4", "permute", or "*" for all --
  * is bracketed by hipEventRecord(events[2n]) before and
  * hipEventRecord(events[2n+1]) after it on the launch stream, for
  * n = count, count + 1, ... < capacity (later launches are not bracketed);
@@ -570,6 +570,132 @@ mok_status mok_linear_forward(const mok_linear_desc* d, const void* x, const voi
 mok_status mok_linear_backward(const mok_linear_desc* d, const void* dy, const void* pre, const void* x, const void* w,
                                const void* dx_add, const void* dw_add, void* dx, void* dw, float* db, void* ws,
                                size_t ws_bytes, void* stream);
+
+/*
+ * Parts that an expert layer is built from, for experts that are not the layer's own (biases, other
+ * activations, fp32, 4-bit weights): rows to the experts' order and back, and matrix products grouped
+ * by expert. mok_route and mok_schedule_build give what they need: offsets[E+1], perm[R] and inv[R] of the
+ * schedule table (mok_schedule_layout) are the `off`, `perm` and `inv` below.
+ */
+
+/*
+ * Matrix products grouped by expert, and their gradients.
+ *   M rows in all (0 <= M < 2^30), E groups (1..1024), K inputs, N outputs, act, epi, P and flags as of
+ *   mok_linear_desc; w has below 2^37 elements, and (M/128 + E) * ceil(max(P,K)/128) and
+ *   E * ceil(P/128) * ceil(K/128) are below 2^24 (MOK_ERR_SHAPE).
+ *   off [E+1] int32 on the device: group e is rows off[e] .. off[e+1]-1, 0 <= off[0] <= ... <=
+ *   off[E] <= M (anything else gives unspecified results inside the arrays). A group may be empty.
+ *   Rows in no group are not read, and those of outputs are left as they were.
+ * The choice of a tile goes by M, E, N and K, as if the rows were spread evenly.
+ */
+typedef struct mok_grouped_desc {
+  int64_t M;
+  int32_t N, K, E;
+  int32_t act;  /* mok_dtype */
+  int32_t epi;  /* mok_epilogue */
+  uint32_t flags;
+  int32_t reserved; /* must be 0 */
+} mok_grouped_desc;
+
+/* Bytes of the workspaces (fwd_ws: 0).  Pure host computation. */
+mok_status mok_grouped_workspace_query(const mok_grouped_desc* d, mok_linear_sizes* sizes);
+
+/*
+ * mok_grouped_forward -- for each row r of group e:  p = x_r w[e]^T + bias[e];  y_r = f(p) + res_r, in fp32,
+ * rounded once.  x [M][K], w [E][P][K], bias [E][P] fp32 or NULL, res [M][N] or NULL (may be the same
+ * array as y), y [M][N], pre [M][P] (p, for the backward) or NULL.  No other overlap is allowed.
+ */
+mok_status mok_grouped_forward(const mok_grouped_desc* d, const void* x, const void* w, const float* bias,
+                               const int32_t* off, const void* res, void* y, void* pre, void* ws, size_t ws_bytes,
+                               void* stream);
+
+/*
+ * mok_grouped_backward -- gradients of L = <dy, y>.  dp = dy f'(pre), rounded to act as mok_linear_backward's:
+ *   dx_r = dp_r w[e] + dx_add_r,  dw[e] = sum_{r in e} dp_r^T x_r + dw_add[e],  db[e] = sum_{r in e} dp_r.
+ * dx [M][K], dw [E][P][K] (fp32 with MOK_FLAG_WGRAD_F32) and db [E][P] fp32 may be NULL: that gradient is
+ * then not formed (w is read for dx only, x for dw only).  dx_add, dw_add may be NULL and may be the
+ * same arrays as dx and dw; no other overlap is allowed.  dw and db are written for empty groups too
+ * (dw_add or 0, and 0).
+ */
+mok_status mok_grouped_backward(const mok_grouped_desc* d, const void* dy, const void* pre, const void* x,
+                                const void* w, const int32_t* off, const void* dx_add, const void* dw_add, void* dx,
+                                void* dw, float* db, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * Matrix products with 4-bit weights and group scales, dense or grouped by expert (serving).
+ *   w[p][k] = s[p][k/group] * (code[p][k] - z[p][k/group]),  codes 0..15, z 0..15 (8 without zero points).
+ *   M, N, K, E, epi, P and their limits as of mok_grouped_desc; group 32, 64 or 128, K a multiple of it;
+ *   act: the type of x, y, res and s; flags 0 (MOK_ERR_SHAPE).
+ *   q [E][P][K/2]: two codes a byte, the even one in the low nibble; s [E][P][K/group] in act;
+ *   z [E][P][K/group] bytes or NULL.
+ */
+typedef struct mok_q4_desc {
+  int64_t M;
+  int32_t N, K, E;
+  int32_t group;
+  int32_t act;  /* mok_dtype */
+  int32_t epi;  /* mok_epilogue */
+  uint32_t flags;
+  int32_t reserved; /* must be 0 */
+} mok_q4_desc;
+
+/* Bytes of the forward workspace.  Pure host computation. */
+mok_status mok_q4_workspace_query(const mok_q4_desc* d, size_t* fwd_ws);
+
+/*
+ * mok_q4_quantize -- codes, scales and (z not NULL) zero points of finite w [E][P][K] in act. For the values v
+ * of a group, in fp32, each division and rint (ties to even) rounded:
+ *   z NULL:  s = max|v| / 7 rounded to act,  code = clamp(rint(v / s) + 8, 0, 15)
+ *   else:    lo = min(v, 0), hi = max(v, 0) over the group,  s = (hi - lo) / 15 rounded to act,
+ *            z = clamp(rint(-lo / s), 0, 15),  code = clamp(rint(v / s) + z, 0, 15)
+ *   s = 0:   z and every code 8.
+ * Run once per set of weights. M is not used.
+ */
+mok_status mok_q4_quantize(const mok_q4_desc* d, const void* w, void* q, void* s, uint8_t* z, void* stream);
+
+/*
+ * mok_q4_forward -- p = x_r w[e]^T + bias[e];  y_r = f(p) + res_r, in fp32, rounded once; w enters as the exact
+ * values of its codes and scales.  off as of mok_grouped_desc; NULL (E = 1 only): one group of all M rows.
+ * x [M][K], bias [E][P] fp32 or NULL, res [M][N] or NULL (may be the same array as y), y [M][N].
+ */
+mok_status mok_q4_forward(const mok_q4_desc* d, const void* x, const void* q, const void* s, const uint8_t* z,
+                          const float* bias, const int32_t* off, const void* res, void* y, void* ws, size_t ws_bytes,
+                          void* stream);
+
+/*
+ * Rows of tokens to the experts' order (dispatch) and back (combine), and their gradients.
+ *   T tokens, k slots each (1..16, T*k < 2^31), R rows (0 <= R < 2^31), H elements a row (a multiple of 8,
+ *   8 .. 2^20), every array below 2^37 elements (MOK_ERR_SHAPE); act: the type of the rows.
+ *   perm [R] int32: slot t*k+j of row r; inv [T][k] int32: row of slot t*k+j. An index outside its range
+ *   (-1) stands for none: a row of no slot (padding), a slot without a row (dropped). No two slots name
+ *   one row, and perm and inv agree (else the rows named twice hold either slot's values).
+ */
+typedef struct mok_permute_desc {
+  int64_t T, R;
+  int32_t H, k;
+  int32_t act;      /* mok_dtype */
+  int32_t reserved; /* must be 0 */
+} mok_permute_desc;
+
+/* mok_dispatch_forward -- xs_r = x[perm_r / k], zeros for a row of no slot.  x [T][H], xs [R][H]. */
+mok_status mok_dispatch_forward(const mok_permute_desc* d, const void* x, const int32_t* perm, void* xs, void* stream);
+
+/* mok_dispatch_backward -- dx_t = dx_add_t + sum_j dxs[inv_tj], slots in order, in fp32, rounded once.
+ * dxs [R][H], dx_add [T][H] or NULL (may be the same array as dx), dx [T][H]. */
+mok_status mok_dispatch_backward(const mok_permute_desc* d, const void* dxs, const int32_t* inv, const void* dx_add,
+                                 void* dx, void* stream);
+
+/* mok_combine_forward -- y_t = res_t + sum_j gate_tj o[inv_tj], slots in order, in fp32, rounded once.
+ * o [R][H], gate [T][k] fp32 or NULL (1), res [T][H] or NULL (may be the same array as y), y [T][H]. */
+mok_status mok_combine_forward(const mok_permute_desc* d, const void* o, const float* gate, const int32_t* inv,
+                               const void* res, void* y, void* stream);
+
+/* mok_combine_backward -- gradients of L = <dy, y>: for the slot s of token t with row r,
+ *   d_o_r = gate_s dy_t,  dgate_s = <dy_t, o_r> (fp32; 0 for a slot without a row).
+ * dgate [T][k] may be NULL (o is then not read); the gradient by res is dy.  Rows of no slot: zeros
+ * with perm, left as they were with perm = NULL.  d_o [R][H] must not overlap another array. */
+mok_status mok_combine_backward(const mok_permute_desc* d, const void* dy, const void* o, const float* gate,
+                                const int32_t* inv, const int32_t* perm, void* d_o, float* dgate, void* stream);
 
 /* Static string naming a status code. */
 const char* mok_status_string(mok_status s);

@@ -101,7 +101,8 @@ hipError_t launch_linear_few(const LinearArgs& a, int act, int epi, hipStream_t 
 hipError_t launch_linear_f32(const LinearArgs& a, int tile, int kind, int epi, hipStream_t s);
 
 // dp = dy f'(pre) (epi != NONE; dp may be nullptr with NONE) and the column sums' parts
-// [linear_db_parts][P] fp32 (nullptr: not formed)
+// [linear_db_parts][P] fp32 (nullptr: not formed), of linear_db_rows rows each
+int linear_db_rows(int64_t M, int N);
 int linear_db_parts(int64_t M, int N);
 hipError_t launch_linear_dpre(const void* dy, const void* pre, int64_t M, int N, int act, int epi, void* dp, float* part,
                               hipStream_t s);

@@ -114,6 +114,27 @@ __device__ __forceinline__ void linear_bias8(const LinearArgs& a, int c, float (
   }
 }
 
+// d = dy of eight columns, p = pre of them (u: of the up columns) -> d = dp (u: of the up columns).
+template <typename T, int EPI>
+__device__ __forceinline__ void linear_dpre8(float (&d)[8], const float (&p)[8], float (&u)[8]) {
+  constexpr bool SW = EPI == MOK_EPI_SWIGLU;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    if constexpr (EPI == MOK_EPI_SILU || SW) {
+      const float s = sigmoid_t<T>(p[i]), f = s * (1.0f + p[i] * (1.0f - s));
+      if constexpr (SW) {
+        const float up = d[i] * p[i] * s;
+        d[i] *= u[i] * f;
+        u[i] = up;
+      } else {
+        d[i] *= f;
+      }
+    } else if constexpr (EPI == MOK_EPI_GELU) {
+      d[i] *= phi_f(p[i]) + p[i] * 0.39894228040143268f * expf(-0.5f * p[i] * p[i]);
+    }
+  }
+}
+
 // out = f(sum of the slices' partial products + bias) + add. A wave takes 64 / SL groups of eight
 // columns; SL lanes a group read every SL-th slice each and add their sums in a tree, so that few rows
 // do not wait for one slice after the other (5 x 4096 of 16 slices: 9.7 us with a lane for all of

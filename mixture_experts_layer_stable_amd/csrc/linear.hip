@@ -29,20 +29,9 @@ __global__ __launch_bounds__(256) void linear_dpre_kernel(const T* __restrict__ 
     load8(dy + m * N + c, d);
     if constexpr (EPI != MOK_EPI_NONE) load8(pre + m * P + c, p);
     if constexpr (SW) load8(pre + m * P + N + c, u);
+    linear_dpre8<T, EPI>(d, p, u);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      if constexpr (EPI == MOK_EPI_SILU || SW) {
-        const float s = sigmoid_t<T>(p[i]), f = s * (1.0f + p[i] * (1.0f - s));
-        if constexpr (SW) {
-          const float up = d[i] * p[i] * s;
-          d[i] *= u[i] * f;
-          u[i] = up;
-        } else {
-          d[i] *= f;
-        }
-      } else if constexpr (EPI == MOK_EPI_GELU) {
-        d[i] *= phi_f(p[i]) + p[i] * 0.39894228040143268f * expf(-0.5f * p[i] * p[i]);
-      }
       sg[i] += d[i];
       if constexpr (SW) su[i] += u[i];
     }
@@ -153,6 +142,8 @@ hipError_t launch_linear(const LinearArgs& args, int kind, int act, int epi, boo
   if (act == MOK_BF16) return launch_linear_bf16(a, p.tile, kind, epi, out_f32, s);
   return launch_linear_f32(a, p.tile, kind, epi, s);
 }
+
+int linear_db_rows(int64_t M, int N) { return (int)dpre_rows(M, N, true); }
 
 int linear_db_parts(int64_t M, int N) {
   if (M == 0) return 0;

@@ -315,36 +315,45 @@ __device__ __forceinline__ void dense_epilogue(f32x16_t (&acc)[Tl::FM][Tl::FN], 
 
 constexpr int kBand = 8;  // tile rows of a band of the tile walk
 
-// PART: the tile's sums over this slice of K go to a.part; linear_join_kernel adds the slices.
-template <typename T, class Tl, int KIND, int EPI, typename TO, bool PART>
-__global__ __launch_bounds__(Tl::NT) void linear_dense_kernel(LinearArgs a) {
-  constexpr bool SW = EPI == MOK_EPI_SWIGLU;
-  // 256 x 256 tiles belong to outputs that no cache keeps: stored past L2, they leave it to the
-  // operands' bands (16384 x (2 x 2048) x 7168: 818 -> 745 us)
-  constexpr bool NTS = Tl::BM * Tl::BN >= 256 * 256;
+// Operands and LDS of a product's workgroup.
+template <typename T, class Tl, int KIND, int EPI>
+struct DenseCfg {
+  static constexpr bool SW = EPI == MOK_EPI_SWIGLU;
   using OA = std::conditional_t<KIND == LIN_DW, DenseMN<T, Tl::BM, Tl::FM, Tl::NW>, DenseK<T, Tl::BM, Tl::FM, Tl::NW>>;
   using OB =
       std::conditional_t<KIND == LIN_FWD, DenseK<T, Tl::BN, Tl::FN, Tl::NW, SW>, DenseMN<T, Tl::BN, Tl::FN, Tl::NW>>;
-  constexpr int64_t ES = sizeof(T), BKE = kRowBytes / ES;
-  constexpr int PATCH = Tl::NW * 32 * kDensePatch * 4;
+  static constexpr int PATCH = Tl::NW * 32 * kDensePatch * 4;
   // B's third LDS stage where as many workgroups of it fit a CU's 160 KB as of two stages (fp32 64 x 64
   // tiles, 1 x 4096 x 4096: 33 -> 25 us; with fewer workgroups it costs more than it gives)
-  constexpr int kCuLds = 160 << 10;
-  constexpr int BST = kCuLds / DenseRing<OA, OB, 3>::BYTES == kCuLds / DenseRing<OA, OB, 2>::BYTES ? 3 : 2;
-  constexpr int RING = DenseRing<OA, OB, BST>::BYTES;
-  __shared__ __align__(1024) char smem[RING > PATCH ? RING : PATCH];
+  static constexpr int kCuLds = 160 << 10;
+  static constexpr int BST = kCuLds / DenseRing<OA, OB, 3>::BYTES == kCuLds / DenseRing<OA, OB, 2>::BYTES ? 3 : 2;
+  static constexpr int RING = DenseRing<OA, OB, BST>::BYTES;
+  static constexpr int LDS = RING > PATCH ? RING : PATCH;
+  static constexpr int BN = SW ? Tl::BN / 2 : Tl::BN;  // outputs of a tile's columns
+  static constexpr int64_t BKE = kRowBytes / (int64_t)sizeof(T);
+};
+
+// Tile r of a band-by-band walk over MT x NT tiles: consecutive ones take a band of kBand tile rows
+// column by column.
+__device__ __forceinline__ void band_walk(int r, int MT, int NT, int& mt, int& nt) {
+  const int band = r / (kBand * NT), gm = min(kBand, MT - band * kBand), i = r - band * kBand * NT;
+  mt = band * kBand + i % gm;
+  nt = i / gm;
+}
+
+// One workgroup's tile at row m0, column n0, over K-tiles kt0 .. kt1-1; rows end at a.M. part: nullptr, or
+// where a slice's sums go (linear_join_kernel adds the slices).
+template <typename T, class Tl, int KIND, int EPI, typename TO, bool PART>
+__device__ __forceinline__ void dense_work(const LinearArgs& a, int64_t m0, int n0, int64_t kt0, int64_t kt1, float* part,
+                                           char* smem) {
+  using Cfg = DenseCfg<T, Tl, KIND, EPI>;
+  constexpr bool SW = Cfg::SW;
+  // 256 x 256 tiles belong to outputs that no cache keeps: stored past L2, they leave it to the
+  // operands' bands (16384 x (2 x 2048) x 7168: 818 -> 745 us)
+  constexpr bool NTS = Tl::BM * Tl::BN >= 256 * 256;
+  constexpr int64_t ES = sizeof(T);
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wm = wave / Tl::WN, wn = wave % Tl::WN;
-  constexpr int BN = SW ? Tl::BN / 2 : Tl::BN;  // outputs of a tile's columns
-  const int NT = (a.N + BN - 1) / BN, MT = (int)((a.M + Tl::BM - 1) / Tl::BM);
-  // tile walk: consecutive workgroups of an XCD take a band of kBand tile rows column by column
-  int L = xcd_logical(blockIdx.x, gridDim.x);
-  const int slice = L / (MT * NT);
-  L -= slice * MT * NT;
-  const int band = L / (kBand * NT), gm = min(kBand, MT - band * kBand), r = L - band * kBand * NT;
-  const int64_t m0 = (int64_t)(band * kBand + r % gm) * Tl::BM;
-  const int n0 = (r / gm) * BN;
-  const int64_t KT = (a.K + BKE - 1) / BKE, kt0 = KT * slice / a.split, kt1 = KT * (slice + 1) / a.split;
 
   const auto frow_a = [&](int f) { return wm * Tl::WTM + f * 32; };
   const auto frow_b = [&](int f) { return wn * Tl::WTN + f * 32; };
@@ -352,8 +361,8 @@ __global__ __launch_bounds__(Tl::NT) void linear_dense_kernel(LinearArgs a) {
   const auto col = [&](int j) { return SW ? n0 + (j / 64) * 32 + (j & 31) : n0 + j; };
   const T* A = (const T*)a.a;
   const T* B = (const T*)a.b;
-  OA oa;
-  OB ob;
+  typename Cfg::OA oa;
+  typename Cfg::OB ob;
   if constexpr (KIND == LIN_DW) {
     oa.init(A + m0, ES * a.M, a.K, a.M - m0, frow_a, wave, lane);
   } else {
@@ -369,11 +378,10 @@ __global__ __launch_bounds__(Tl::NT) void linear_dense_kernel(LinearArgs a) {
   }
   f32x16_t acc[Tl::FM][Tl::FN];
   zero_acc<Tl>(acc);
-  if (kt1 > kt0) dense_loop<T, Tl, BST>(oa, ob, kt0, kt1, smem, wave, acc);
+  if (kt1 > kt0) dense_loop<T, Tl, Cfg::BST>(oa, ob, kt0, kt1, smem, wave, acc);
 
   const auto in = [&](int row, int j) { return m0 + row < a.M && col(j) < a.N; };
   if constexpr (PART) {
-    float* part = a.part + (int64_t)slice * a.M * (SW ? 2 * a.N : a.N);
     dense_epilogue<Tl, SW>(
         acc, smem, wave, wm, wn, lane, [](int, int) { return 0; },
         [&](auto, int row, int j, float (&g)[8], float (&u)[8], int) {
@@ -408,6 +416,19 @@ __global__ __launch_bounds__(Tl::NT) void linear_dense_kernel(LinearArgs a) {
         }
         if (in(row, j)) linear_store8<KIND, EPI, TO, T, NTS>(a, m0 + row, col(j), g, u, add);
       });
+}
+
+template <typename T, class Tl, int KIND, int EPI, typename TO, bool PART>
+__global__ __launch_bounds__(Tl::NT) void linear_dense_kernel(LinearArgs a) {
+  using Cfg = DenseCfg<T, Tl, KIND, EPI>;
+  __shared__ __align__(1024) char smem[Cfg::LDS];
+  const int NT = (a.N + Cfg::BN - 1) / Cfg::BN, MT = (int)((a.M + Tl::BM - 1) / Tl::BM);
+  int L = xcd_logical(blockIdx.x, gridDim.x), mt, nt;
+  const int slice = L / (MT * NT);
+  band_walk(L - slice * MT * NT, MT, NT, mt, nt);
+  const int64_t KT = (a.K + Cfg::BKE - 1) / Cfg::BKE, kt0 = KT * slice / a.split, kt1 = KT * (slice + 1) / a.split;
+  dense_work<T, Tl, KIND, EPI, TO, PART>(a, (int64_t)mt * Tl::BM, nt * Cfg::BN, kt0, kt1,
+                                         a.part + (int64_t)slice * a.M * (Cfg::SW ? 2 * a.N : a.N), smem);
 }
 
 template <typename T, class Tl, int KIND, int EPI, typename TO>

@@ -101,6 +101,23 @@ class _LinearSizes(ctypes.Structure):
     _fields_ = [("fwd_ws", ctypes.c_size_t), ("bwd_ws", ctypes.c_size_t)]
 
 
+class _GroupedDesc(ctypes.Structure):
+    _fields_ = [("M", ctypes.c_int64), ("N", ctypes.c_int32), ("K", ctypes.c_int32), ("E", ctypes.c_int32),
+                ("act", ctypes.c_int32), ("epi", ctypes.c_int32), ("flags", ctypes.c_uint32),
+                ("reserved", ctypes.c_int32)]
+
+
+class _Q4Desc(ctypes.Structure):
+    _fields_ = [("M", ctypes.c_int64), ("N", ctypes.c_int32), ("K", ctypes.c_int32), ("E", ctypes.c_int32),
+                ("group", ctypes.c_int32), ("act", ctypes.c_int32), ("epi", ctypes.c_int32), ("flags", ctypes.c_uint32),
+                ("reserved", ctypes.c_int32)]
+
+
+class _PermuteDesc(ctypes.Structure):
+    _fields_ = [("T", ctypes.c_int64), ("R", ctypes.c_int64), ("H", ctypes.c_int32), ("k", ctypes.c_int32),
+                ("act", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+
+
 MX_LAYOUT_FIELDS = ("fwd_slot", "xq", "xs", "hq", "hs", "bwd_slot", "dyq", "dys", "dguq", "dgus", "st_xs", "st_dos",
                     "st_h", "st_dgu", "pofs", "dot", "dots", "ht", "hts", "dgut", "dguts", "xt", "xts")
 
@@ -138,6 +155,16 @@ def _load():
         "mok_linear_workspace_query": [ctypes.POINTER(_LinearDesc), ctypes.POINTER(_LinearSizes)],
         "mok_linear_forward": [ctypes.POINTER(_LinearDesc)] + [P] * 7 + [Z, P],
         "mok_linear_backward": [ctypes.POINTER(_LinearDesc)] + [P] * 10 + [Z, P],
+        "mok_grouped_workspace_query": [ctypes.POINTER(_GroupedDesc), ctypes.POINTER(_LinearSizes)],
+        "mok_grouped_forward": [ctypes.POINTER(_GroupedDesc)] + [P] * 8 + [Z, P],
+        "mok_grouped_backward": [ctypes.POINTER(_GroupedDesc)] + [P] * 11 + [Z, P],
+        "mok_q4_workspace_query": [ctypes.POINTER(_Q4Desc), ctypes.POINTER(Z)],
+        "mok_q4_quantize": [ctypes.POINTER(_Q4Desc)] + [P] * 5,
+        "mok_q4_forward": [ctypes.POINTER(_Q4Desc)] + [P] * 9 + [Z, P],
+        "mok_dispatch_forward": [ctypes.POINTER(_PermuteDesc)] + [P] * 4,
+        "mok_dispatch_backward": [ctypes.POINTER(_PermuteDesc)] + [P] * 5,
+        "mok_combine_forward": [ctypes.POINTER(_PermuteDesc)] + [P] * 6,
+        "mok_combine_backward": [ctypes.POINTER(_PermuteDesc)] + [P] * 8,
     }
     for name, args in sig.items():
         f = getattr(lib, name)
@@ -157,7 +184,10 @@ EXPORTS = ("mok_workspace_query", "mok_schedule_layout_query", "mok_saved_layout
            "mok_weights_quantize", "mok_status_string", "mok_version", "mok_trace_bind",
            "mok_norm_workspace_query", "mok_rmsnorm_forward", "mok_rmsnorm_backward",
            "mok_balance_workspace_query", "mok_balance_forward", "mok_balance_backward",
-           "mok_linear_workspace_query", "mok_linear_forward", "mok_linear_backward")
+           "mok_linear_workspace_query", "mok_linear_forward", "mok_linear_backward",
+           "mok_grouped_workspace_query", "mok_grouped_forward", "mok_grouped_backward",
+           "mok_q4_workspace_query", "mok_q4_quantize", "mok_q4_forward",
+           "mok_dispatch_forward", "mok_dispatch_backward", "mok_combine_forward", "mok_combine_backward")
 NOALLOC_WS_BYTES = 32 << 20
 
 
@@ -552,6 +582,171 @@ def linear_backward(d: LinearDesc, dy, x, w, dx=None, dw=None, db=None, pre=None
          _ptr("w", w, t, (P, K), dev, dx is None), _ptr("dx_add", dx_add, t, (M, K), dev, True),
          _ptr("dw_add", dw_add, wt, (P, K), dev, True), _ptr("dx", dx, t, (M, K), dev, True),
          _ptr("dw", dw, wt, (P, K), dev, True), _ptr("db", db, torch.float32, (P,), dev, True), wp, wn)
+
+
+@dataclass(frozen=True)
+class GroupedDesc:
+    """y_r = f(x_r w[e]^T + bias[e]) + res_r for the rows r of E groups e (mok_grouped_desc); x [M, K], y [M, N]."""
+    M: int
+    N: int
+    K: int
+    E: int
+    act: int = BF16
+    epi: int = EPI_NONE
+    flags: int = 0
+
+    def __post_init__(self):
+        object.__setattr__(self, "_c", _GroupedDesc(self.M, self.N, self.K, self.E, self.act, self.epi, self.flags, 0))
+
+    def c(self) -> _GroupedDesc:
+        return self._c
+
+    @property
+    def P(self) -> int:
+        """Columns of a product (rows of a group's w)."""
+        return 2 * self.N if self.epi == EPI_SWIGLU else self.N
+
+
+def grouped_workspace_query(d: GroupedDesc) -> dict:
+    s = _LinearSizes()
+    _check(_lib.mok_grouped_workspace_query(d._c, s), "mok_grouped_workspace_query")
+    return dict(fwd_ws=s.fwd_ws, bwd_ws=s.bwd_ws)
+
+
+def grouped_forward(d: GroupedDesc, x, w, off, y, bias=None, res=None, pre=None, ws=None, stream=None):
+    """pre = x w[e]^T + bias[e]; y = f(pre) + res for the rows off[e] .. off[e + 1] - 1 of each group e."""
+    M, N, K, E, P, t, dev = d.M, d.N, d.K, d.E, d.P, TORCH_DTYPE.get(d.act), _dev("x", x)
+    wp, wn = _ws(ws, dev)
+    _run(_lib.mok_grouped_forward, "mok_grouped_forward", dev, stream, d._c, _ptr("x", x, t, (M, K), dev),
+         _ptr("w", w, t, (E, P, K), dev), _ptr("bias", bias, torch.float32, (E, P), dev, True),
+         _ptr("off", off, torch.int32, (E + 1,), dev), _ptr("res", res, t, (M, N), dev, True),
+         _ptr("y", y, t, (M, N), dev), _ptr("pre", pre, t, (M, P), dev, True), wp, wn)
+
+
+def grouped_backward(d: GroupedDesc, dy, x, w, off, dx=None, dw=None, db=None, pre=None, dx_add=None, dw_add=None,
+                     ws=None, stream=None):
+    """dp = dy f'(pre); dx = dp w[e] + dx_add, dw[e] = sum dp^T x + dw_add[e], db[e] = sum dp over the rows of group e
+    (each only when its tensor is given)."""
+    M, N, K, E, P, t, dev = d.M, d.N, d.K, d.E, d.P, TORCH_DTYPE.get(d.act), _dev("dy", dy)
+    wt = torch.float32 if d.flags & FLAG_WGRAD_F32 else t
+    if (dx_add is not None and dx is None) or (dw_add is not None and dw is None):
+        raise ValueError("dx_add, dw_add: without the gradient that they are added to")
+    wp, wn = _ws(ws, dev)
+    _run(_lib.mok_grouped_backward, "mok_grouped_backward", dev, stream, d._c, _ptr("dy", dy, t, (M, N), dev),
+         _ptr("pre", pre, t, (M, P), dev, d.epi == EPI_NONE), _ptr("x", x, t, (M, K), dev, dw is None),
+         _ptr("w", w, t, (E, P, K), dev, dx is None), _ptr("off", off, torch.int32, (E + 1,), dev),
+         _ptr("dx_add", dx_add, t, (M, K), dev, True), _ptr("dw_add", dw_add, wt, (E, P, K), dev, True),
+         _ptr("dx", dx, t, (M, K), dev, True), _ptr("dw", dw, wt, (E, P, K), dev, True),
+         _ptr("db", db, torch.float32, (E, P), dev, True), wp, wn)
+
+
+@dataclass(frozen=True)
+class Q4Desc:
+    """Products with 4-bit weights w = s (code - z), one scale (and zero point) per `group` codes along K
+    (mok_q4_desc); E matrices, dense with E = 1."""
+    M: int
+    N: int
+    K: int
+    E: int = 1
+    group: int = 128
+    act: int = BF16
+    epi: int = EPI_NONE
+    flags: int = 0
+
+    def __post_init__(self):
+        object.__setattr__(self, "_c", _Q4Desc(self.M, self.N, self.K, self.E, self.group, self.act, self.epi, self.flags,
+                                               0))
+
+    def c(self) -> _Q4Desc:
+        return self._c
+
+    @property
+    def P(self) -> int:
+        """Columns of a product (rows of a matrix)."""
+        return 2 * self.N if self.epi == EPI_SWIGLU else self.N
+
+
+def q4_workspace_query(d: Q4Desc) -> dict:
+    n = ctypes.c_size_t()
+    _check(_lib.mok_q4_workspace_query(d._c, n), "mok_q4_workspace_query")
+    return dict(fwd_ws=n.value)
+
+
+def _q4_shapes(d: Q4Desc):
+    g = max(d.group, 1)
+    return (d.E, d.P, d.K // 2), (d.E, d.P, d.K // g)
+
+
+def q4_quantize(d: Q4Desc, w, q, s, z=None, stream=None):
+    """Codes q [E, P, K/2] (two a byte, the even one low), scales s [E, P, K/group] and, when given, zero points
+    z (bytes) of w [E, P, K]."""
+    t, dev = TORCH_DTYPE.get(d.act), _dev("w", w)
+    qs, ss = _q4_shapes(d)
+    _run(_lib.mok_q4_quantize, "mok_q4_quantize", dev, stream, d._c, _ptr("w", w, t, (d.E, d.P, d.K), dev),
+         _ptr("q", q, torch.uint8, qs, dev), _ptr("s", s, t, ss, dev), _ptr("z", z, torch.uint8, ss, dev, True))
+
+
+def q4_forward(d: Q4Desc, x, q, s, y, z=None, off=None, bias=None, res=None, ws=None, stream=None):
+    """y = f(x w[e]^T + bias[e]) + res with 4-bit w, for the rows off[e] .. off[e + 1] - 1 of each group e (off = None,
+    with E = 1 only: all rows)."""
+    M, N, K, E, t, dev = d.M, d.N, d.K, d.E, TORCH_DTYPE.get(d.act), _dev("x", x)
+    qs, ss = _q4_shapes(d)
+    wp, wn = _ws(ws, dev)
+    _run(_lib.mok_q4_forward, "mok_q4_forward", dev, stream, d._c, _ptr("x", x, t, (M, K), dev),
+         _ptr("q", q, torch.uint8, qs, dev), _ptr("s", s, t, ss, dev), _ptr("z", z, torch.uint8, ss, dev, True),
+         _ptr("bias", bias, torch.float32, (E, d.P), dev, True), _ptr("off", off, torch.int32, (E + 1,), dev, E == 1),
+         _ptr("res", res, t, (M, N), dev, True), _ptr("y", y, t, (M, N), dev), wp, wn)
+
+
+@dataclass(frozen=True)
+class PermuteDesc:
+    """T tokens of k slots and R rows of H elements in the experts' order (mok_permute_desc); R = None: T * k."""
+    T: int
+    H: int
+    k: int
+    R: Optional[int] = None
+    act: int = BF16
+
+    def __post_init__(self):
+        if self.R is None:
+            object.__setattr__(self, "R", self.T * self.k)
+        object.__setattr__(self, "_c", _PermuteDesc(self.T, self.R, self.H, self.k, self.act, 0))
+
+    def c(self) -> _PermuteDesc:
+        return self._c
+
+
+def dispatch_forward(d: PermuteDesc, x, perm, xs, stream=None):
+    """xs[r] = x[perm[r] / k], zeros where perm[r] names no slot."""
+    t, dev = TORCH_DTYPE.get(d.act), _dev("x", x)
+    _run(_lib.mok_dispatch_forward, "mok_dispatch_forward", dev, stream, d._c, _ptr("x", x, t, (d.T, d.H), dev),
+         _ptr("perm", perm, torch.int32, (d.R,), dev), _ptr("xs", xs, t, (d.R, d.H), dev))
+
+
+def dispatch_backward(d: PermuteDesc, dxs, inv, dx, add=None, stream=None):
+    """dx[t] = add[t] + sum_j dxs[inv[t, j]]."""
+    t, dev, rows = TORCH_DTYPE.get(d.act), _dev("dxs", dxs), (d.T, d.H)
+    _run(_lib.mok_dispatch_backward, "mok_dispatch_backward", dev, stream, d._c, _ptr("dxs", dxs, t, (d.R, d.H), dev),
+         _ptr("inv", inv, torch.int32, (d.T, d.k), dev), _ptr("add", add, t, rows, dev, True), _ptr("dx", dx, t, rows, dev))
+
+
+def combine_forward(d: PermuteDesc, o, inv, y, gate=None, res=None, stream=None):
+    """y[t] = res[t] + sum_j gate[t, j] o[inv[t, j]]."""
+    t, dev, rows = TORCH_DTYPE.get(d.act), _dev("o", o), (d.T, d.H)
+    _run(_lib.mok_combine_forward, "mok_combine_forward", dev, stream, d._c, _ptr("o", o, t, (d.R, d.H), dev),
+         _ptr("gate", gate, torch.float32, (d.T, d.k), dev, True), _ptr("inv", inv, torch.int32, (d.T, d.k), dev),
+         _ptr("res", res, t, rows, dev, True), _ptr("y", y, t, rows, dev))
+
+
+def combine_backward(d: PermuteDesc, dy, o, inv, do, gate=None, dgate=None, perm=None, stream=None):
+    """do[r] = gate[s] dy[t] and dgate[s] = <dy[t], o[r]> for the slot s of token t with row r; with perm, rows of no
+    slot get zeros."""
+    t, dev, rows = TORCH_DTYPE.get(d.act), _dev("dy", dy), (d.R, d.H)
+    slots = (d.T, d.k)
+    _run(_lib.mok_combine_backward, "mok_combine_backward", dev, stream, d._c, _ptr("dy", dy, t, (d.T, d.H), dev),
+         _ptr("o", o, t, rows, dev, dgate is None), _ptr("gate", gate, torch.float32, slots, dev, True),
+         _ptr("inv", inv, torch.int32, slots, dev), _ptr("perm", perm, torch.int32, (d.R,), dev, True),
+         _ptr("do", do, t, rows, dev), _ptr("dgate", dgate, torch.float32, slots, dev, True))
 
 
 class KernelTrace:
