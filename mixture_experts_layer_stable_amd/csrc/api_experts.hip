@@ -235,11 +235,13 @@ mok_status mok_q4_forward(const mok_q4_desc* d, const void* x, const void* q, co
   a.l.add = res;
   a.l.out = y;
   a.s = s;
-  a.z = z;
+  a.z = z != nullptr ? z : (const uint8_t*)s;
+  a.zeros = z != nullptr;
   a.off = off;
   a.E = d->E;
   a.group = d->group;
-  MOK_LAUNCH("q4", (hipStream_t)stream, launch_q4(a, d->act, d->epi, (hipStream_t)stream));
+  a.epi = d->epi;
+  MOK_LAUNCH("q4", (hipStream_t)stream, launch_q4(a, d->act, (hipStream_t)stream));
   return MOK_OK;
 }
 

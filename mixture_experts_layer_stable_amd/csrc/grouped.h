@@ -15,74 +15,65 @@ struct GroupTile {
   int tiles;  // of the group
 };
 
+// Inclusive sum over the lanes of a wave.
+__device__ __forceinline__ int wave_scan(int v) {
+  v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xf, 0xf, false);  // row_shr:1, 2, 4, 8
+  v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xf, 0xf, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xf, 0xf, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xf, 0xf, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xa, 0xf, false);  // row_bcast:15 to rows 1 and 3
+  v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xc, 0xf, false);  // row_bcast:31 to rows 2 and 3
+  return v;
+}
+
 // The groups cut into tiles of bm rows: a lane holds 1/64 of the groups, the wave a prefix sum of
 // their tiles, so a tile is found in one round of loads wherever it lies (a table of tiles would be a
 // launch of its own, 3 us). Every wave of the workgroup does so for itself.
 struct GroupScan {
-  int v[17];   // offsets of this lane's groups
-  int excl;    // tiles before them
-  int total;   // tiles of all groups
+  const int32_t* off;
   int C, M, E, g0;
+  int excl;   // tiles before this lane's groups
+  int total;  // tiles of all groups
 
-  __device__ __forceinline__ void init(const int32_t* __restrict__ off, int E_, int64_t M_, int bm) {
-    const int lane = threadIdx.x & 63;
+  // at most: group_tiles_bound, which offsets that descend could pass
+  __device__ __forceinline__ void init(const int32_t* __restrict__ off_, int E_, int64_t M_, int bm) {
+    off = off_;
     E = E_;
     M = (int)M_;
     C = (E + 63) >> 6;
-    g0 = lane * C;
-#pragma unroll
-    for (int c = 0; c < 17; ++c)
-      if (c <= C) v[c] = off[min(g0 + c, E)];
-    // offsets that descend count as the largest before them, so that the groups' rows are at most M
-    int top = 0;
-#pragma unroll
-    for (int c = 0; c < 17; ++c)
-      if (c <= C) top = group_clamp(v[c], top, M);
-#pragma unroll
-    for (int o = 1; o < 64; o <<= 1) {
-      const int t = __shfl_up(top, o);
-      if (lane >= o) top = max(top, t);
+    g0 = (threadIdx.x & 63) * C;
+    int lo = group_clamp(off[min(g0, E)], 0, M), n = 0;
+#pragma unroll 4
+    for (int c = 1; c <= C; ++c) {
+      const int hi = group_clamp(off[min(g0 + c, E)], lo, M);
+      n += (int)((uint32_t)(hi - lo + bm - 1) / (uint32_t)bm);
+      lo = hi;
     }
-    const int before = __shfl_up(top, 1);
-    v[0] = group_clamp(v[0], lane == 0 ? 0 : before, M);
-    int n = 0;
-#pragma unroll
-    for (int c = 0; c < 16; ++c)
-      if (c < C) {
-        v[c + 1] = group_clamp(v[c + 1], v[c], M);
-        n += (v[c + 1] - v[c] + bm - 1) / bm;
-      }
-    int incl = n;
-#pragma unroll
-    for (int o = 1; o < 64; o <<= 1) {
-      const int t = __shfl_up(incl, o);
-      if (lane >= o) incl += t;
-    }
+    n = min(n, 1 << 24);
+    const int incl = wave_scan(n);
     excl = incl - n;
-    total = __builtin_amdgcn_readlane(incl, 63);
+    total = min(__builtin_amdgcn_readlane(incl, 63), M / bm + min(E, M));
   }
 
   // The group of tile q, 0 <= q < total.
   __device__ __forceinline__ GroupTile find(int q, int bm) const {
-    int g = 0, lo = 0, hi = 0, first = 0, tiles = 0, at = excl;
+    GroupTile f{0, 0, 0, 0, 0};
+    int lo = group_clamp(off[min(g0, E)], 0, M), at = excl;
     bool here = false;
-#pragma unroll
-    for (int c = 0; c < 16; ++c)
-      if (c < C) {
-        const int t = (v[c + 1] - v[c] + bm - 1) / bm;
-        if (q >= at && q < at + t) {
-          here = true;
-          g = g0 + c;
-          lo = v[c];
-          hi = v[c + 1];
-          first = at;
-          tiles = t;
-        }
-        at += t;
+#pragma unroll 4
+    for (int c = 1; c <= C; ++c) {
+      const int hi = group_clamp(off[min(g0 + c, E)], lo, M);
+      const int t = (int)((uint32_t)(hi - lo + bm - 1) / (uint32_t)bm);
+      if (q >= at && q < at + t) {
+        here = true;
+        f = {g0 + c - 1, lo, hi, at, t};
       }
+      at += t;
+      lo = hi;
+    }
     const int src = __builtin_ctzll(__ballot(here));
-    return {__builtin_amdgcn_readlane(g, src), __builtin_amdgcn_readlane(lo, src), __builtin_amdgcn_readlane(hi, src),
-            __builtin_amdgcn_readlane(first, src), __builtin_amdgcn_readlane(tiles, src)};
+    return {__builtin_amdgcn_readlane(f.g, src), __builtin_amdgcn_readlane(f.lo, src), __builtin_amdgcn_readlane(f.hi, src),
+            __builtin_amdgcn_readlane(f.first, src), __builtin_amdgcn_readlane(f.tiles, src)};
   }
 };
 

@@ -73,9 +73,6 @@ hipError_t launch_q4_quantize(const void* w, int64_t rows, int K, int group, int
   return hipGetLastError();
 }
 
-hipError_t launch_q4(const Q4Args& a, int act, int epi, hipStream_t s) {
-  const int rt = a.l.M <= 16 * (int64_t)std::min<int64_t>(a.E, a.l.M) ? 1 : 2;
-  return launch_q4_few(a, rt, act, epi, s);
-}
+hipError_t launch_q4(const Q4Args& a, int act, hipStream_t s) { return launch_q4_few(a, act, s); }
 
 }  // namespace mok

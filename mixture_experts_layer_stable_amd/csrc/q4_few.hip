@@ -2,12 +2,16 @@
 //
 //   p[m][n] = sum over groups j of K of s[n][j] (sum_k x[m][k] (16 + q[n][k]) - (16 + z[n][j]) sum_k x[m][k])
 //
-// What bounds them is the codes' way from HBM and its latency, so a workgroup takes 16 rows of w (8 gate
-// and 8 up rows for SWIGLU) over all of K, as linear_few.hip, and its eight waves take 128 codes of K
-// of each row in turn. A code becomes a matrix operand without arithmetic: 16 + q in bf16 is
-// 0x4180 | q << 3, two of a dword at a time; the products are exact in fp32, a multiplication by ones
-// gives the sums of x that the offset brought in, in the lanes that hold the results, and a group's
-// result takes its scale in fp32. So w is never rounded to bf16. fp32 x: codes as fp32 numbers q - z.
+// What bounds them is the codes' way from HBM, its latency, and next the instructions that a code takes. A
+// wave takes 16 rows of w (8 gate and 8 up rows for SWIGLU) and 128 codes of each at a time; four such
+// pieces are on their way while the four before them are worked on. Of a workgroup's eight waves WS share
+// a row tile, each a part of K, and 8 / WS tiles lie side by side. The workgroups, two a CU, share the tiles
+// of all groups evenly; a workgroup's rows of x stay in LDS for all of its tiles (or pass through it in two
+// stages), in the order in which the matrix units want them, so a wave streams codes from tile to tile.
+// A code becomes a matrix operand without arithmetic: 16 + q in bf16 is 0x4180 | q << 3, two of a dword at
+// a time. A second multiplication, by -(16 + z), takes off what the offset brought in; both are exact in
+// fp32 up to its sums, and a group's result takes its scale in fp32. So w is never rounded to bf16.
+// fp32 x: codes as fp32 numbers q - z.
 #include "linear_few.h"
 #include "q4.h"
 
@@ -16,8 +20,14 @@ namespace mok {
 namespace {
 
 constexpr int kPiece = 128;  // codes of a row that a wave takes at a time
+constexpr int kBatch = 4;    // pieces that it loads at a time
+constexpr int kWaves = 8;
+constexpr int kRows = 16;    // rows of x of a workgroup
 
-// Lanes l, l + 16, l + 32, l + 48 hold four units each: unit d of lane group g <-> unit g of lane group d.
+// A barrier for what the waves left in LDS. __syncthreads would wait for the codes that are on their way, too.
+__device__ __forceinline__ void lds_barrier() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
+
+// Lanes l, l + 16, l + 32, l + 48 hold four dwords each: dword d of lane group g <-> dword g of lane group d.
 __device__ __forceinline__ void swap32(uint32_t& a, uint32_t& b) {
   const auto r = __builtin_amdgcn_permlane32_swap(a, b, false, false);
   a = r[0];
@@ -28,15 +38,11 @@ __device__ __forceinline__ void swap16(uint32_t& a, uint32_t& b) {
   a = r[0];
   b = r[1];
 }
-template <int W>
-__device__ __forceinline__ void group_transpose(uint32_t (&u)[4][W]) {
-#pragma unroll
-  for (int i = 0; i < W; ++i) {
-    swap32(u[0][i], u[2][i]);
-    swap32(u[1][i], u[3][i]);
-    swap16(u[0][i], u[1][i]);
-    swap16(u[2][i], u[3][i]);
-  }
+__device__ __forceinline__ void group_transpose(uint32_t (&u)[4]) {
+  swap32(u[0], u[2]);
+  swap32(u[1], u[3]);
+  swap16(u[0], u[1]);
+  swap16(u[2], u[3]);
 }
 
 // Eight codes of a dword as bf16 16 + q, in the order 0 4 1 5 2 6 3 7.
@@ -50,203 +56,288 @@ __device__ __forceinline__ uint4 order_bf16(const uint4& x) {
                     __builtin_amdgcn_perm(x.w, x.y, 0x05040100u), __builtin_amdgcn_perm(x.w, x.y, 0x07060302u));
 }
 
-// RT: tiles of 16 rows of x; G: codes that share a scale
-template <typename T, int EPI, int RT, int G>
-__global__ __launch_bounds__(64 * kFewWaves) void q4_few_kernel(Q4Args qa) {
-  constexpr bool SW = EPI == MOK_EPI_SWIGLU, BF = std::is_same<T, bf16>::value;
-  constexpr int BM = 16 * RT, XV = sizeof(T) / 2;  // 16-byte vectors of eight values of x
+// G: codes that share a scale; WS: waves that share a tile of w
+template <typename T, bool SW, int G, int WS>
+__global__ __launch_bounds__(64 * kWaves) void q4_few_kernel(Q4Args qa) {
+  constexpr bool BF = std::is_same<T, bf16>::value;
+  constexpr int WN = kWaves / WS, NTH = 64 * kWaves;
+  constexpr int XV = BF ? 1 : 2;                   // 16-byte vectors of eight values of x
   constexpr int GP = kPiece / G;                   // scales of a piece
-  constexpr int NB = RT == 1 && BF ? 4 : 2;        // pieces that a wave loads at a time
-  __shared__ __align__(16) float s_sum[kFewWaves][BM][kFewLd];
+  constexpr uint32_t XB = 128 << 10;               // of x in LDS, or twice a stage of it
+  constexpr int NX = XB / 2 / 16 / NTH;            // vectors of a stage that a thread loads
+  __shared__ __align__(16) struct {
+    char x[XB];
+    float sum[kWaves][kRows][kFewLd];
+  } lds;
   LinearArgs a = qa.l;
-  const int NT = SW ? a.N / 8 : (a.N + 15) / 16;
-  int L;
-  GroupTile t;
-  if (!q4_tile(qa, BM, NT, L, t)) return;
-  const int i0 = L - t.first * NT, mt = i0 % t.tiles, nt = i0 / t.tiles;
-  const int64_t r0 = t.lo + (int64_t)mt * BM, P = SW ? 2 * (int64_t)a.N : a.N;
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, r = lane & 15, g = lane >> 4;
-  const int n0 = nt * (SW ? 8 : 16), K = (int)a.K, M = (int)min<int64_t>(BM, t.hi - r0), KG = K / G;
-  // row of w of this lane (rows past N re-read the last one)
-  const int64_t wr = t.g * P + (SW ? (r < 8 ? n0 + r : (int64_t)a.N + n0 + r - 8) : min(n0 + r, a.N - 1));
-  const uint8_t* wq = (const uint8_t*)a.b + wr * (K / 2);
-  const T* ws = (const T*)qa.s + wr * KG;
-  const uint8_t* wz = qa.z != nullptr ? qa.z + wr * KG : nullptr;
-  // x: register j of a lane is of row 4 (r / 4) + j until quad_transpose, as in linear_few.hip
-  const T* x[RT][4];
-#pragma unroll
-  for (int q = 0; q < RT; ++q)
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int m = 16 * q + (r & 12) + j;
-      x[q][j] = m < M ? (const T*)a.a + (r0 + m) * K : nullptr;
-    }
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int r = lane & 15, g = lane >> 4, ks = wave % WS;
+  const uint32_t K = (uint32_t)a.K, KG = K / G, pieces = (K + kPiece - 1) / kPiece, rounds = (pieces + WS - 1) / WS;
+  const int64_t P = SW ? 2 * (int64_t)a.N : a.N;
+  const int cols = SW ? 8 : 16, NS = ((a.N + cols - 1) / cols + WN - 1) / WN;  // sets of WN tiles of w
 
-  struct Batch {
-    uint4 w[NB];
-    uint4 x[NB][RT][XV][4];
-    float s[GP], z[GP];  // of piece (lane group) of the batch
-  };
-  const int pieces = (K + kPiece - 1) / kPiece, rounds = (pieces + kFewWaves - 1) / kFewWaves;
-  const int first = (int)((nt >> 3 & 31) * (unsigned)pieces >> 5);  // workgroups start all over K
-  // first code of piece `i` of this wave, or K for none
-  const auto at = [&](int i) {
-    int q = i * kFewWaves + wave;
-    if (q >= pieces) return K;
-    q += first;
-    return (q >= pieces ? q - pieces : q) * kPiece;
-  };
-  const auto load = [&](int i, Batch& b) {
-#pragma unroll
-    for (int n = 0; n < NB; ++n) {
-      const int k = at(i + n) + 32 * g;
-      b.w[n] = k < K ? ldg16(wq + k / 2) : make_uint4(0, 0, 0, 0);
-#pragma unroll
-      for (int q = 0; q < RT; ++q)
-#pragma unroll
-        for (int h = 0; h < XV; ++h)
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const int e = k + (BF ? 8 * (r & 3) : 16 * h + 4 * (r & 3));
-            b.x[n][q][h][j] = k < K && x[q][j] != nullptr ? ldg16(x[q][j] + e) : make_uint4(0, 0, 0, 0);
-          }
-    }
-    const int k = g < NB ? at(i + g) : K;
-#pragma unroll
-    for (int p = 0; p < GP; ++p) {
-      const bool in = k + p * G < K;
-      b.s[p] = in ? Elem<T>::get(ws, k / G + p) : 0.0f;
-      b.z[p] = in && wz != nullptr ? (float)wz[k / G + p] : 8.0f;
-    }
-  };
-  f32x4_t acc[RT];
-#pragma unroll
-  for (int q = 0; q < RT; ++q) acc[q] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
-  const f32x4_t zero = {0.0f, 0.0f, 0.0f, 0.0f};
-  const auto mma = [&](Batch& b) {
-#pragma unroll
-    for (int n = 0; n < NB; ++n) {
-      uint32_t w[4][1] = {{b.w[n].x}, {b.w[n].y}, {b.w[n].z}, {b.w[n].w}};
-      if constexpr (GP > 1) group_transpose(w);
-      float sc[GP], zp[GP];
-#pragma unroll
-      for (int p = 0; p < GP; ++p) {
-        sc[p] = __shfl(b.s[p], r + 16 * n);
-        zp[p] = __shfl(b.z[p], r + 16 * n);
+  // this workgroup's sets: an even share of those of all row tiles
+  int cur = 0, end = 1;
+  for (bool begin = true; cur < end; begin = false) {
+    GroupTile t;
+    int q;
+    {
+      GroupScan scan;
+      int total = ((int)a.M + kRows - 1) / kRows;
+      if (qa.off != nullptr) {
+        scan.init(qa.off, qa.E, a.M, kRows);
+        total = scan.total;
       }
+      if (begin) {
+        const int all = total * NS, wgs = min(all, (int)gridDim.x);
+        if ((int)blockIdx.x >= wgs) return;
+        const int l = xcd_logical(blockIdx.x, wgs), share = all / wgs, more = all - share * wgs;
+        cur = l * share + min(l, more);
+        end = cur + share + (l < more);
+      }
+      q = cur / NS;
+      t = {0, 0, (int)a.M, 0, total};
+      if (qa.off != nullptr) t = scan.find(q, kRows);
+    }
+    // row tile and sets of it: set0 ..
+    const int set0 = cur - q * NS, nset = min(end - cur, NS - set0);
+    cur += nset;
+    const int64_t r0 = t.lo + (int64_t)(q - t.first) * kRows;
+    const uint32_t M = (uint32_t)min<int64_t>(kRows, t.hi - r0);
+    const T* x = (const T*)a.a + r0 * K;
+
+    // x in LDS: 2^mb rows of SP pieces; eight values (unit u of a piece) are a lane's for one step: step
+    // u % 4 of lane group u / 4 if the piece has one scale, else, as group_transpose leaves the codes, step
+    // u / 4 of lane group u % 4. Rows past M hold what was there: it ends in results that are not stored.
+    int mb = 0;
+    while ((1u << mb) < M) ++mb;
+    const uint32_t pb = (16 * 16 * XV) << mb;  // bytes of a piece
+    const bool staged = pieces * pb > XB;
+    const uint32_t XR = staged ? XB / 2 / pb / WS : rounds, SP = staged ? XR * WS : pieces;  // rounds, pieces of a stage
+    const auto slot = [&](uint32_t p, uint32_t step, uint32_t h, uint32_t lg, uint32_t m) {  // of 16 bytes
+      return ((((p * 4 + step) * XV + h) * 4 + lg) << mb) + ((m ^ (4 * lg + step)) & ((1u << mb) - 1));
+    };
+    // 64 vectors of a row of the pieces from p0 on: block i of M * nb, nb blocks a row
+    const auto get_x = [&](uint32_t p0, uint32_t i, uint32_t nb) {
+      const uint32_t m = i / nb, c = (i - m * nb) * 64 + lane, k = p0 * kPiece + c * (8 / XV);
+      const uint4 d = ldg16(x + (uint64_t)min(m, M - 1) * K + min(k, K - 8 / XV));
+      return k < K ? d : make_uint4(0, 0, 0, 0);
+    };
+    const auto put_x = [&](char* to, uint32_t i, uint32_t nb, uint32_t n, uint4 d) {
+      const uint32_t m = i / nb, c = (i - m * nb) * 64 + lane, u = c / XV % 16, h = c % XV;
+      if constexpr (BF) d = order_bf16(d);
+      if (m < M && c < n)
+        *reinterpret_cast<uint4*>(to + 16 * slot(c / (16 * XV), GP > 1 ? u / 4 : u % 4, h, GP > 1 ? u % 4 : u / 4, m)) = d;
+    };
+    const uint32_t sv = SP * (16 * XV), sb = (sv + 63) / 64;  // vectors and blocks of a row of a stage
+    const uint32_t stages = (pieces + SP - 1) / SP;
+    uint4 xr[NX];
+    const auto load_x = [&](uint32_t st) {
 #pragma unroll
-      for (int q = 0; q < RT; ++q) {
-        uint32_t u[4][4 * XV];
+      for (int i = 0; i < NX; ++i) xr[i] = get_x(st * SP, i * kWaves + wave, sb);
+    };
+    const auto store_x = [&](uint32_t buf) {
 #pragma unroll
-        for (int h = 0; h < XV; ++h) {
-          quad_transpose(b.x[n][q][h]);
+      for (int i = 0; i < NX; ++i) put_x(lds.x + (buf & 1) * (XB / 2), i * kWaves + wave, sb, sv, xr[i]);
+    };
+    uint32_t xoff[4];
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            // bf16: vector j is unit j; fp32: vectors 2 (j % 2) .. of half h are unit 2 h + j / 2
-            const uint4& v = b.x[n][q][h][j];
-            const int d = BF ? j : 2 * h + j / 2, o = BF ? 0 : 4 * (j % 2);
-            u[d][o] = v.x;
-            u[d][o + 1] = v.y;
-            u[d][o + 2] = v.z;
-            u[d][o + 3] = v.w;
+    for (int e = 0; e < 4; ++e) xoff[e] = 16 * slot(0, e, 0, g, r);
+    const uint32_t xhalf = 16 * 4 << mb;  // to the second vector
+
+    // Codes and scales of a batch: of piece n, and of piece (lane group). Every load is made, whatever the piece:
+    // behind a condition the compiler would not know how many are on their way, and wait for all of them;
+    // for the same reason scales stay as loaded. Past the end the last codes come again, with a scale of 0.
+    struct Batch {
+      uint4 w[kBatch];
+      T s[GP];
+      uint8_t z[GP];
+      bool in[GP];
+    };
+    int set_l = set0;
+    uint32_t round_l = 0;  // the loads' place in the stream
+    const uint8_t *wq, *wz;
+    const T* ws;
+    const auto rows_l = [&]() {
+      const int n0 = (set_l * WN + wave / WS) * cols;  // rows past N re-read the last one
+      const int64_t wr = t.g * P + (SW ? (int64_t)min(n0 + (r & 7), a.N - 1) + (r < 8 ? 0 : a.N) : min(n0 + r, a.N - 1));
+      wq = (const uint8_t*)a.b + wr * (K / 2);
+      ws = (const T*)qa.s + wr * KG;
+      wz = qa.z + wr * KG;
+    };
+    const int last = set0 + nset - 1;
+    const auto load = [&](Batch& d) {
+#pragma unroll
+      for (int n = 0; n < kBatch; ++n) {
+        const uint32_t p = min((round_l + n) * WS + ks, pieces - 1);
+        d.w[n] = ldg16(wq + min(p * (kPiece / 2) + 16 * g, K / 2 - 16));
+      }
+      const uint32_t p = (round_l + g) * WS + ks;
+#pragma unroll
+      for (int j = 0; j < GP; ++j) {
+        const uint32_t i = p * GP + j;
+        d.in[j] = p < pieces && i < KG;
+        d.s[j] = ws[d.in[j] ? i : 0];
+        d.z[j] = wz[d.in[j] ? i : 0];
+      }
+      round_l += kBatch;
+      if (round_l >= rounds) {
+        round_l = 0;
+        set_l = min(set_l + 1, last);
+        rows_l();
+      }
+    };
+    f32x4_t acc = {0.0f, 0.0f, 0.0f, 0.0f};
+    int set = set0;
+    uint32_t round = 0, sc = 0, buf_round = 0;  // of the work; stages gone by; round within the stage
+    const auto work = [&](const Batch& d) {
+      float ds[GP];
+      uint32_t dz[GP];
+#pragma unroll
+      for (int j = 0; j < GP; ++j) {
+        ds[j] = d.in[j] ? Elem<T>::get(&d.s[j], 0) : 0.0f;
+        // bf16: -(16 + z) twice; fp32: z
+        if constexpr (BF) dz[j] = 0xC180C180u | (qa.zeros ? d.z[j] & 15u : 8u) * 0x00080008u;
+        else dz[j] = __float_as_uint(qa.zeros ? (float)d.z[j] : 8.0f);
+      }
+      static_for<0, kBatch>([&](auto nc) {
+        constexpr int n = decltype(nc)::value;
+        if (staged) {
+          if (buf_round == XR && round + n < rounds) {  // the next stage of x
+            ++sc;
+            store_x(sc);
+            lds_barrier();
+            load_x((sc + 1) % stages);
+            buf_round = 0;
           }
+          ++buf_round;
         }
-        if constexpr (GP > 1) group_transpose(u);
+        const uint32_t p = min((round + n) * WS + ks, pieces - 1);
+        const char* xs = lds.x + (staged ? (sc & 1) * (XB / 2) + min(p - sc % stages * SP, SP - 1) * pb : p * pb);
+        uint32_t w[4] = {d.w[n].x, d.w[n].y, d.w[n].z, d.w[n].w};
+        if constexpr (GP > 1) group_transpose(w);
 #pragma unroll
-        for (int p = 0; p < GP; ++p) {
-          f32x4_t d = zero, o = zero;
+        for (int j = 0; j < GP; ++j) {
+          const float s = __shfl(ds[j], r + 16 * n);
+          const uint32_t z = __shfl(dz[j], r + 16 * n);
+          f32x4_t dd = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-          for (int e = p * (4 / GP); e < (p + 1) * (4 / GP); ++e) {
+          for (int e = j * (4 / GP); e < (j + 1) * (4 / GP); ++e) {
+            const uint4 xv = *reinterpret_cast<const uint4*>(xs + xoff[e]);
             if constexpr (BF) {
-              const uint4 xv = order_bf16(make_uint4(u[e][0], u[e][1], u[e][2], u[e][3]));
-              const uint4 one = make_uint4(0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u);
-              d = mma16<bf16>(xv, codes_bf16(w[e][0]), d);
-              o = mma16<bf16>(xv, one, o);
+              dd = mma16<bf16>(xv, make_uint4(z, z, z, z), dd);
+              dd = mma16<bf16>(xv, codes_bf16(w[e]), dd);
             } else {
-              const uint32_t lo = w[e][0] & 0x0F0F0F0Fu, hi = w[e][0] >> 4 & 0x0F0F0F0Fu;
+              const uint4 xw = *reinterpret_cast<const uint4*>(xs + xhalf + xoff[e]);
+              const uint32_t lo = w[e] & 0x0F0F0F0Fu, hi = w[e] >> 4 & 0x0F0F0F0Fu;
+              const uint32_t xa[8] = {xv.x, xv.y, xv.z, xv.w, xw.x, xw.y, xw.z, xw.w};
 #pragma unroll
               for (int c = 0; c < 8; ++c) {
-                const float wv = (float)((c & 1 ? hi : lo) >> (8 * (c / 2)) & 0xFFu) - zp[p];
-                d = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(u[e][c % (4 * XV)]), wv, d, 0, 0, 0);
+                const float f = (float)((c & 1 ? hi : lo) >> (8 * (c / 2)) & 0xFFu) - __uint_as_float(z);
+                dd = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(xa[c]), f, dd, 0, 0, 0);
               }
             }
           }
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-            acc[q][i] = __builtin_fmaf(sc[p], BF ? __builtin_fmaf(-16.0f - zp[p], o[i], d[i]) : d[i], acc[q][i]);
+          for (int c = 0; c < 4; ++c) acc[c] = __builtin_fmaf(s, dd[c], acc[c]);
         }
+      });
+      round += kBatch;
+      if (round < rounds) return;
+      // y of the tiles of the set: a thread (of the wave, or of the workgroup) finishes eight outputs of a row
+      constexpr int TPR = SW ? 1 : 2;
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        lds.sum[wave][4 * g + c][r] = acc[c];
+        acc[c] = 0.0f;
       }
+      if constexpr (WS > 1) lds_barrier();
+      else __builtin_amdgcn_wave_barrier();
+      const int v = WS > 1 ? tid : lane;
+      const int tile = WS > 1 ? v / (kRows * TPR) : wave, row = v / TPR % kRows, h = SW ? 0 : 8 * (v % TPR);
+      const int c0 = (set * WN + tile) * cols + h;
+      if (v < (WS > 1 ? WN : 1) * kRows * TPR && row < (int)M && c0 < a.N) {
+        const Raw8<T> add = linear_add8<T>(a, r0 + row, c0);
+        float s[8], u[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) s[i] = u[i] = 0.0f;
+#pragma unroll
+        for (int k = 0; k < WS; ++k) {
+          float f[8];
+          load8(&lds.sum[tile * WS + k][row][h], f);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) s[i] += f[i];
+          if constexpr (SW) {
+            load8(&lds.sum[tile * WS + k][row][8], f);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) u[i] += f[i];
+          }
+        }
+        q4_finish<T, SW>(a, a.bias != nullptr ? a.bias + t.g * P : nullptr, qa.epi, r0 + row, c0, s, u, add);
+      }
+      if constexpr (WS > 1) lds_barrier();
+      else __builtin_amdgcn_wave_barrier();
+      round = 0;
+      ++set;
+      if (staged) buf_round = XR;  // the next set begins with the first stage
+    };
+
+    Batch b0, b1;
+    rows_l();
+    load(b0);
+    lds_barrier();  // the rows before these are done with
+    if (staged) {
+      load_x(0);
+      store_x(0);
+      load_x(1);
+    } else {
+#pragma unroll 2
+      for (uint32_t i = wave; i < M * sb; i += kWaves) put_x(lds.x, i, sb, sv, get_x(0, i, sb));
     }
-  };
-  Batch b0, b1;
-  load(0, b0);
-  // what this lane stores in the end: eight outputs of a row, and what is added to them
-  const int row = SW ? tid : tid >> 1, c = n0 + (SW ? 0 : 8 * (tid & 1));
-  const bool out = row < M && c < a.N;
-  Raw8<T> add{};
-  float bg[8], bu[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) bg[i] = bu[i] = 0.0f;
-  if (a.bias != nullptr) a.bias += t.g * P;
-  if (out) {
-    add = linear_add8<T>(a, r0 + row, c);
-    linear_bias8<EPI>(a, c, bg, bu);
+    lds_barrier();
+    while (true) {
+      load(b1);
+      work(b0);
+      if (set > last) break;
+      load(b0);
+      work(b1);
+      if (set > last) break;
+    }
   }
-  for (int i = 0; i < rounds; i += 2 * NB) {
-    if (i + NB < rounds) load(i + NB, b1);
-    mma(b0);
-    if (i + NB >= rounds) break;
-    if (i + 2 * NB < rounds) load(i + 2 * NB, b0);
-    mma(b1);
-  }
-#pragma unroll
-  for (int q = 0; q < RT; ++q)
-#pragma unroll
-    for (int i = 0; i < 4; ++i) s_sum[wave][16 * q + 4 * g + i][r] = acc[q][i];
-  __syncthreads();
-  if (tid < 256 * RT) {
-    float v = 0.0f;
-#pragma unroll
-    for (int i = 0; i < kFewWaves; ++i) v += s_sum[i][tid >> 4][tid & 15];
-    s_sum[0][tid >> 4][tid & 15] = v;
-  }
-  __syncthreads();
-  if (!out) return;
-  float p[8], u[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    p[i] = s_sum[0][row][(SW ? 0 : c - n0) + i] + bg[i];
-    u[i] = SW ? s_sum[0][row][8 + i] + bu[i] : 0.0f;
-  }
-  linear_store8<LIN_FWD, EPI, T, T>(a, r0 + row, c, p, u, add);
 }
 
-template <typename T, int EPI, int RT>
+// A tile of w for each wave where they are enough for the chip's 256 CUs, else more waves on one.
+template <typename T, bool SW, int G>
 void run_few(const Q4Args& a, hipStream_t s) {
-  const int cols = EPI == MOK_EPI_SWIGLU ? 8 : 16;
-  const dim3 grid((unsigned)(q4_tiles_bound(a, 16 * RT) * ((a.l.N + cols - 1) / cols))), block(64 * kFewWaves);
-  if (a.group == 32) hipLaunchKernelGGL((q4_few_kernel<T, EPI, RT, 32>), grid, block, 0, s, a);
-  else if (a.group == 64) hipLaunchKernelGGL((q4_few_kernel<T, EPI, RT, 64>), grid, block, 0, s, a);
-  else hipLaunchKernelGGL((q4_few_kernel<T, EPI, RT, 128>), grid, block, 0, s, a);
+  const int64_t nt = SW ? a.l.N / 8 : (a.l.N + 15) / 16, mt = q4_tiles_bound(a, kRows);
+  const auto go = [&](auto ws) {
+    constexpr int WS = decltype(ws)::value, WN = kWaves / WS;
+    const int64_t sets = mt * ((nt + WN - 1) / WN);
+    hipLaunchKernelGGL((q4_few_kernel<T, SW, G, WS>), dim3((unsigned)std::min<int64_t>(sets, 256)), dim3(64 * kWaves), 0,
+                       s, a);
+  };
+  if (nt * mt >= 4096) go(std::integral_constant<int, 1>());
+  else if (nt * mt >= 1024) go(std::integral_constant<int, 2>());
+  else go(std::integral_constant<int, 8>());
 }
 
-template <typename T, int RT>
-void run_few(const Q4Args& a, int epi, hipStream_t s) {
-  if (epi == MOK_EPI_NONE) run_few<T, MOK_EPI_NONE, RT>(a, s);
-  else if (epi == MOK_EPI_SILU) run_few<T, MOK_EPI_SILU, RT>(a, s);
-  else if (epi == MOK_EPI_GELU) run_few<T, MOK_EPI_GELU, RT>(a, s);
-  else run_few<T, MOK_EPI_SWIGLU, RT>(a, s);
+template <typename T, bool SW>
+void run_few(const Q4Args& a, hipStream_t s) {
+  if (a.group == 32) run_few<T, SW, 32>(a, s);
+  else if (a.group == 64) run_few<T, SW, 64>(a, s);
+  else run_few<T, SW, 128>(a, s);
 }
 
 }  // namespace
 
-hipError_t launch_q4_few(const Q4Args& a, int rt, int act, int epi, hipStream_t s) {
+hipError_t launch_q4_few(const Q4Args& a, int act, hipStream_t s) {
+  const bool sw = a.epi == MOK_EPI_SWIGLU;
   if (act == MOK_F32) {
-    if (rt == 1) run_few<float, 1>(a, epi, s);
-    else run_few<float, 2>(a, epi, s);
+    if (sw) run_few<float, true>(a, s);
+    else run_few<float, false>(a, s);
   } else {
-    if (rt == 1) run_few<bf16, 1>(a, epi, s);
-    else run_few<bf16, 2>(a, epi, s);
+    if (sw) run_few<bf16, true>(a, s);
+    else run_few<bf16, false>(a, s);
   }
   return hipGetLastError();
 }
