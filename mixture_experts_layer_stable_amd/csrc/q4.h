@@ -15,6 +15,7 @@ struct Q4Args {
 };
 hipError_t launch_q4(const Q4Args& a, int act, hipStream_t s);
 hipError_t launch_q4_few(const Q4Args& a, int act, hipStream_t s);
+hipError_t launch_q4_tile(const Q4Args& a, int act, int bm, hipStream_t s);  // bm: rows of x of a tile, 128 or 256
 hipError_t launch_q4_quantize(const void* w, int64_t rows, int K, int group, int act, void* q, void* s, uint8_t* z,
                               hipStream_t st);
 

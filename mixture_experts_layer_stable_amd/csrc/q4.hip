@@ -73,6 +73,10 @@ hipError_t launch_q4_quantize(const void* w, int64_t rows, int K, int group, int
   return hipGetLastError();
 }
 
-hipError_t launch_q4(const Q4Args& a, int act, hipStream_t s) { return launch_q4_few(a, act, s); }
+hipError_t launch_q4(const Q4Args& a, int act, hipStream_t s) {
+  const int64_t rows = a.l.M / std::min<int64_t>(a.E, a.l.M);
+  if (rows < 64) return launch_q4_few(a, act, s);
+  return launch_q4_tile(a, act, rows < 256 ? 128 : 256, s);
+}
 
 }  // namespace mok
