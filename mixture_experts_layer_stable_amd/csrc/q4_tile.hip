@@ -22,15 +22,16 @@ template <typename T, class Tl, bool SW>
 struct Q4Tile {
   using OA = DenseK<T, Tl::BM, Tl::FM, Tl::NW>;
   static constexpr int BN = 128;
-  static constexpr int kA = 3, kRaw = 4;                  // stages
+  static constexpr bool BF = std::is_same<T, bf16>::value;
+  static constexpr int kA = BF ? 2 : 3, kRaw = BF ? 2 : 4;  // stages
   static constexpr int RAW = 4096 + 1024 + 1024;          // codes, scales, zero points of a K-tile
-  static constexpr int A0 = 0, B0 = kA * OA::BYTES, R0 = B0 + 2 * BN * 128, LDS = R0 + kRaw * RAW;
+  static constexpr int B0 = kA * OA::BYTES, R0 = B0 + 2 * BN * 128, LDS = R0 + kRaw * RAW;
   static constexpr int NL = OA::NI + 3;                   // loads of a wave and K-tile
   static_assert(Tl::BN == BN && Tl::NT == 256 && Tl::FN == 2, "tile");
 };
 
 template <typename T, class Tl, bool SW, int G>
-__global__ __launch_bounds__(Tl::NT) void q4_tile_kernel(Q4Args qa) {
+__global__ __launch_bounds__(Tl::NT, sizeof(T) == 2 ? 2 : 1) void q4_tile_kernel(Q4Args qa) {
   using C = Q4Tile<T, Tl, SW>;
   constexpr bool BF = std::is_same<T, bf16>::value;
   constexpr int ES = sizeof(T), BK = 128 / ES;      // values of a K-tile
@@ -125,68 +126,169 @@ __global__ __launch_bounds__(Tl::NT) void q4_tile_kernel(Q4Args qa) {
       foff[f][ks] = row * 128 + 16 * ((2 * ks + (lane >> 5)) ^ swz_k(row));
     }
 
-  f32x16_t acc[Tl::FM][2], grp[Tl::FM][2];  // fp32: grp is not used
+  f32x16_t acc[Tl::FM][2];
   zero_acc<Tl>(acc);
-  if constexpr (BF) zero_acc<Tl>(grp);
   const uint32_t KT = (K + BK - 1) / BK;
-  // acc += scale * grp for the group that ends in K-tile kt (group h of it)
-  const auto flush = [&](uint32_t kt, int h) {
+  if constexpr (!BF) {
+    // Loads of K-tile kt: x two K-tiles ahead, codes three (past the end: again the last ones, which no one reads).
+    const auto issue = [&](uint32_t kt_a, uint32_t kt_raw) {
+      oa.template issue<false>(min(kt_a, KT - 1), lds + kt_a % C::kA * C::OA::BYTES, wave);
+      issue_raw(kt_raw);
+    };
+    issue_raw(0);
+    issue(0, 1);
+    issue(1, 2);
+    wait_vmcnt<2 * C::NL>();
+    ring_barrier();
+    operand(0);
+    for (uint32_t kt = 0; kt < KT; ++kt) {
+      wait_vmcnt<C::NL>();
+      asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+      issue(kt + 2, kt + 3);
+      const char* sa = smem + kt % C::kA * C::OA::BYTES;
+      const char* sb = smem + C::B0 + (kt & 1) * (C::BN * 128);
+      operand(kt + 1);
 #pragma unroll
-    for (int f = 0; f < 2; ++f) {
-      const int j = wn * Tl::WTN + f * 32 + (lane & 31);
-      const uint32_t i = (uint32_t)wrow(j) * KG + min(kt * BK / G + h, KG - 1);
-      const uint32_t sr = *reinterpret_cast<const uint32_t*>(smem + C::R0 + kt % C::kRaw * C::RAW + 4096 + 4 * (2 * j + h));
-      const float s = __uint_as_float(sr >> ((i & 1) * 16) << 16);
+      for (int ks = 0; ks < 4; ++ks) {
+        uint4 fa[Tl::FM], fb[2];
 #pragma unroll
-      for (int m = 0; m < Tl::FM; ++m)
+        for (int f = 0; f < 2; ++f) fb[f] = *reinterpret_cast<const uint4*>(sb + foff[f][ks]);
 #pragma unroll
-        for (int r = 0; r < 16; ++r) {
-          acc[m][f][r] = __builtin_fmaf(s, grp[m][f][r], acc[m][f][r]);
-          grp[m][f][r] = 0.0f;
-        }
+        for (int m = 0; m < Tl::FM; ++m) fa[m] = oa.frag(sa, m, ks);
+#pragma unroll
+        for (int m = 0; m < Tl::FM; ++m)
+#pragma unroll
+          for (int f = 0; f < 2; ++f) Mma<T>::run(acc[m][f], fa[m], fb[f]);
+      }
     }
-  };
-
-  // Loads of K-tile kt: x two K-tiles ahead, codes three (past the end: again the last ones, which no one reads).
-  const auto issue = [&](uint32_t kt_a, uint32_t kt_raw) {
-    const uint32_t to = lds + C::A0 + kt_a % C::kA * C::OA::BYTES;
-    oa.template issue<false>(min(kt_a, KT - 1), to, wave);
-    issue_raw(kt_raw);
-  };
-  issue_raw(0);
-  issue(0, 1);
-  issue(1, 2);
-  wait_vmcnt<2 * C::NL>();
-  ring_barrier();
-  operand(0);
-  for (uint32_t kt = 0; kt < KT; ++kt) {
-    wait_vmcnt<C::NL>();
+  } else {
+    // One wave a SIMD: everything has its place between two matrix instructions, as in dense_tile. At a
+    // K-tile's last step the wave holds its fragments of it: it waits for its loads of the next and for
+    // the workgroup, reads the next one's first fragments and loads x two, codes three K-tiles ahead. In
+    // the other steps the next K-tile's codes become operands. A group's sums go to acc where the next
+    // group's first products would overwrite them.
+    constexpr int NM = Tl::FM * 2, NR = Tl::FM + 2;
+    f32x16_t grp[Tl::FM][2];
+    zero_acc<Tl>(grp);
+    uint4 fa[2][Tl::FM], fb[2][2];
+    uint32_t sr[2][2] = {{0, 0}, {0, 0}};  // [half of the K-tile][f]: scales as loaded, of the group that ends there
+    uint32_t sh[2] = {0, 0};               // [f]: low bits of the index of column f's first scale
+#pragma unroll
+    for (int f = 0; f < 2; ++f) sh[f] = (uint32_t)wrow(wn * Tl::WTN + f * 32 + (lane & 31)) * KG;
+    float s[2] = {0.0f, 0.0f};  // of the group that ended last
+    const auto read_scales = [&](const char* raw, uint32_t (&to)[2][2]) {
+#pragma unroll
+      for (int f = 0; f < 2; ++f) {
+        const char* p = raw + 4096 + 8 * (wn * Tl::WTN + f * 32 + (lane & 31));
+        to[0][f] = *reinterpret_cast<const uint32_t*>(p);
+        if constexpr (G == 32) to[1][f] = *reinterpret_cast<const uint32_t*>(p + 4);
+      }
+    };
+    const auto flush = [&](auto ic) {
+      constexpr int i = decltype(ic)::value, m = i / 2, f = i % 2;
+#pragma unroll
+      for (int r = 0; r < 16; ++r) acc[m][f][r] = __builtin_fmaf(s[f], grp[m][f][r], acc[m][f][r]);
+    };
+    const auto step = [&](auto fullc, uint32_t kt) {
+      constexpr bool FULL = decltype(fullc)::value;
+      const uint32_t nk = kt + 1;
+      const char* raw = smem + C::R0 + nk % C::kRaw * C::RAW;
+      char* to = smem + C::B0 + (nk & 1) * (C::BN * 128) + brow * 128;
+      uint4 w;
+      uint32_t zr = 0;
+      float z = 0.0f;
+      uint32_t lo = 0, hi = 0;
+      uint32_t op[4], srn[2][2];
+      const uint32_t kd = kt + 2, dst = lds + kd % C::kA * C::OA::BYTES;
+      static_for<0, 4>([&](auto kc) {
+        constexpr int ks = decltype(kc)::value, c = ks & 1;
+        constexpr bool first = G == 32 ? ks % 2 == 0 : ks == 0;  // of a group, or of half of one of 128
+        if constexpr (ks == 3) {
+          wait_vmcnt<0>();
+          asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+        }
+        const char* sa = smem + (ks == 3 ? nk : kt) % C::kA * C::OA::BYTES;
+        const char* sb = smem + C::B0 + ((ks == 3 ? nk : kt) & 1) * (C::BN * 128);
+        static_for<0, NM>([&](auto ic) {
+          constexpr int i = decltype(ic)::value, m = i / 2, f = i % 2, slot = ks * NM + i;
+          if constexpr (first) {
+            flush(ic);
+            const f32x16_t zero = {};
+            grp[m][f] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8_t, fa[c][m]),
+                                                                __builtin_bit_cast(bf16x8_t, fb[c][f]), zero, 0, 0, 0);
+          } else {
+            Mma<T>::run(grp[m][f], fa[c][m], fb[c][f]);
+          }
+          if constexpr (i < NR) {
+            if constexpr (i < 2) fb[c ^ 1][i] = *reinterpret_cast<const uint4*>(sb + foff[i][(ks + 1) & 3]);
+            else fa[c ^ 1][i - 2] = oa.frag(sa, i - 2, (ks + 1) & 3);
+          }
+          // the next K-tile's operands: 32 codes, two at a time from slot 4 on
+          if constexpr (slot == 0) {
+            w = *reinterpret_cast<const uint4*>(raw + 16 * tid);
+            zr = *reinterpret_cast<const uint32_t*>(raw + 4096 + 1024 + 4 * tid);
+          }
+          constexpr int kFirst = NM == 8 ? 4 : 1, kPer = NM == 8 ? 1 : 2;  // first slot, pairs a slot
+          if constexpr (slot == kFirst) {
+            const uint32_t ix = sg_lo + min(nk * BK / G + (GP > 1 ? part : 0), KG - 1);
+            z = qa.zeros ? (float)(zr >> ((ix & 3) * 8) & 0xFFu) : 8.0f;
+          }
+          if constexpr (slot >= kFirst && slot < kFirst + 16 / kPer) {
+            static_for<0, kPer>([&](auto pc) {
+              constexpr int pair = (slot - kFirst) * kPer + decltype(pc)::value, u = pair / 4, q = pair % 4;
+              if constexpr (q == 0) {
+                const uint32_t wd = u == 0 ? w.x : (u == 1 ? w.y : (u == 2 ? w.z : w.w));
+                lo = wd & 0x0F0F0F0Fu;
+                hi = wd >> 4 & 0x0F0F0F0Fu;
+              }
+              op[q] = bf16x2_rne((float)(lo >> (8 * q) & 0xFFu) - z, (float)(hi >> (8 * q) & 0xFFu) - z);
+              if constexpr (q == 3)
+                *reinterpret_cast<uint4*>(to + 16 * ((4 * part + u) ^ swz_k(brow))) = make_uint4(op[0], op[1], op[2], op[3]);
+            });
+          }
+          // scales of the groups that end in the next K-tile; of the group that has just ended
+          if constexpr (slot == NM) read_scales(raw, srn);
+          if constexpr (i == NM - 1 && (ks == 3 || (G == 32 && ks == 1))) {
+#pragma unroll
+            for (int ff = 0; ff < 2; ++ff) {
+              const uint32_t ix = sh[ff] + min(kt * BK / G + (G == 32 && ks == 3 ? 1 : 0), KG - 1);
+              s[ff] = __uint_as_float(sr[G == 32 && ks == 3][ff] >> ((ix & 1) * 16) << 16);
+            }
+          }
+          if constexpr (slot == 4 * NM - 1) {
+#pragma unroll
+            for (int h = 0; h < (G == 32 ? 2 : 1); ++h)
+#pragma unroll
+              for (int ff = 0; ff < 2; ++ff) sr[h][ff] = srn[h][ff];
+          }
+          if constexpr (ks == 3) {
+            constexpr int NI = C::OA::NI;
+            oa.template issue<FULL>(FULL ? kd : min(kd, KT - 1), dst, wave, i * NI / NM, (i + 1) * NI / NM);
+            if constexpr (i == NM - 1) issue_raw(kt + 3);
+          }
+          __builtin_amdgcn_sched_barrier(0);
+        });
+      });
+    };
+    issue_raw(0);
+    issue_raw(1);
+    oa.template issue<false>(0, lds, wave);
+    wait_vmcnt<0>();
+    ring_barrier();
+    operand(0);
+    read_scales(smem + C::R0, sr);
     asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
-    issue(kt + 2, kt + 3);
-    const char* sa = smem + C::A0 + kt % C::kA * C::OA::BYTES;
-    const char* sb = smem + C::B0 + (kt & 1) * (C::BN * 128);
-    operand(kt + 1);
+    oa.template issue<false>(min(1u, KT - 1), lds + C::OA::BYTES, wave);
+    issue_raw(2);
 #pragma unroll
-    for (int ks = 0; ks < 4; ++ks) {
-      uint4 fa[Tl::FM], fb[2];
+    for (int m = 0; m < Tl::FM; ++m) fa[0][m] = oa.frag(smem, m, 0);
 #pragma unroll
-      for (int f = 0; f < 2; ++f) fb[f] = *reinterpret_cast<const uint4*>(sb + foff[f][ks]);
-#pragma unroll
-      for (int m = 0; m < Tl::FM; ++m) fa[m] = oa.frag(sa, m, ks);
-#pragma unroll
-      for (int m = 0; m < Tl::FM; ++m)
-#pragma unroll
-        for (int f = 0; f < 2; ++f) {
-          if constexpr (BF) Mma<T>::run(grp[m][f], fa[m], fb[f]);
-          else Mma<T>::run(acc[m][f], fa[m], fb[f]);
-        }
-      if constexpr (BF && G == 32)
-        if (ks == 1) flush(kt, 0);
-    }
-    if constexpr (BF) {
-      if (G == 32) flush(kt, 1);
-      else if (((kt + 1) * BK) % G == 0 || kt + 1 == KT) flush(kt, 0);
-    }
+    for (int f = 0; f < 2; ++f) fb[0][f] = *reinterpret_cast<const uint4*>(smem + C::B0 + foff[f][0]);
+    uint32_t kt = 0;
+    for (const uint32_t full = (uint32_t)oa.full(); kt + 2 < full; ++kt) step(std::true_type(), kt);
+#pragma unroll 1
+    for (; kt < KT; ++kt) step(std::false_type(), kt);
+    static_for<0, NM>([&](auto ic) { flush(ic); });
   }
   wait_vmcnt<0>();
   __syncthreads();
@@ -203,7 +305,7 @@ __global__ __launch_bounds__(Tl::NT) void q4_tile_kernel(Q4Args qa) {
       for (int r = 0; r < 16; ++r)
         patch[(8 * (r >> 2) + 4 * (lane >> 5) + (r & 3)) * kDensePatch + 32 * f + (lane & 31)] = acc[m][f][r];
     __builtin_amdgcn_wave_barrier();
-#pragma unroll
+#pragma unroll 1
     for (int i = 0; i < LPR / 2; ++i) {
       const int row = lane / LPR + (64 / LPR) * i, c = (lane % LPR) * 8;
       const int mm = wm * Tl::WTM + m * 32 + row, cc = col(wn * Tl::WTN + c);
@@ -238,7 +340,6 @@ void run_tile(const Q4Args& a, hipStream_t s) {
 
 hipError_t launch_q4_tile(const Q4Args& a, int act, int bm, hipStream_t s) {
   if (act == MOK_F32) run_tile<float, Tiling<128, 128, 2, 2>>(a, s);
-  else if (bm == 256) run_tile<bf16, Tiling<256, 128, 2, 2>>(a, s);
   else run_tile<bf16, Tiling<128, 128, 2, 2>>(a, s);
   return hipGetLastError();
 }
