@@ -190,7 +190,8 @@ mok_status mok_q4_workspace_query(const mok_q4_desc* d, size_t* fwd_ws) {
   mok_status st = check_q4(d);
   if (st != MOK_OK) return st;
   if (fwd_ws == nullptr) return MOK_ERR_NULL;
-  *fwd_ws = 0;
+  const int split = d->E == 1 ? q4_split(d->act, d->epi, d->M, d->N, d->K, 1) : 0;
+  *fwd_ws = split > 1 ? up(4 * (size_t)split * (size_t)d->M * (d->epi == MOK_EPI_SWIGLU ? 2 * d->N : d->N)) : 0;
   return MOK_OK;
 }
 
@@ -234,6 +235,7 @@ mok_status mok_q4_forward(const mok_q4_desc* d, const void* x, const void* q, co
   a.l.bias = bias;
   a.l.add = res;
   a.l.out = y;
+  a.l.part = (float*)ws;
   a.s = s;
   a.z = z != nullptr ? z : (const uint8_t*)s;
   a.zeros = z != nullptr;

@@ -15,7 +15,9 @@ struct Q4Args {
 };
 hipError_t launch_q4(const Q4Args& a, int act, hipStream_t s);
 hipError_t launch_q4_few(const Q4Args& a, int act, hipStream_t s);
-hipError_t launch_q4_tile(const Q4Args& a, int act, int bm, hipStream_t s);  // bm: rows of x of a tile, 128 or 256
+hipError_t launch_q4_tile(const Q4Args& a, int act, hipStream_t s);
+// Slices of K in tiles of 128 x 128, or 0: q4_few.hip. A function of the shape and type only.
+int q4_split(int act, int epi, int64_t M, int N, int K, int E);
 hipError_t launch_q4_quantize(const void* w, int64_t rows, int K, int group, int act, void* q, void* s, uint8_t* z,
                               hipStream_t st);
 

@@ -73,10 +73,40 @@ hipError_t launch_q4_quantize(const void* w, int64_t rows, int K, int group, int
   return hipGetLastError();
 }
 
-hipError_t launch_q4(const Q4Args& a, int act, hipStream_t s) {
-  const int64_t rows = a.l.M / std::min<int64_t>(a.E, a.l.M);
-  if (rows < 64) return launch_q4_few(a, act, s);
-  return launch_q4_tile(a, act, rows < 256 ? 128 : 256, s);
+// The faster of the two kernels by estimates (us) fitted to shapes from 1 to 4096 rows. q4_few.hip: what 16 rows
+// of a group take for a million codes. Tiles: K-tiles (of 64, fp32 32) one after the other, half as long on
+// an empty chip as on a full one, in rounds of 512 (fp32 256); slices of K, of a dense product only (a second
+// launch that adds them would have to know the rows' groups), cost their partial products' way to memory and back.
+int q4_split(int act, int epi, int64_t M, int N, int K, int E) {
+  if (M == 0) return 0;
+  const bool f32 = act == MOK_F32;
+  const double P = epi == MOK_EPI_SWIGLU ? 2.0 * N : N, groups = (double)std::min<int64_t>(E, M);
+  const double row_tiles = std::max(groups, (double)M / 16 + 0.5 * groups), rows = (double)M / groups;
+  double least = 6.0 + row_tiles * P * K * 1e-6 * (f32 ? 0.75 : (rows > 4 ? 0.38 : 0.2));
+  int best = 0;
+  const double tiles = std::max(groups, (double)M / 128 + 0.5 * groups) * std::max(1.0, P / 128), slots = f32 ? 256 : 512;
+  const int pieces = (K + 127) / 128;
+  for (int split = 1; split <= (E == 1 ? 64 : 1); split *= 2) {
+    if (split > 1 && (pieces / split < 2 || tiles * split >= 4096)) break;
+    const double fill = std::min(1.0, tiles * split / slots), kts = (double)((pieces + split - 1) / split) * (f32 ? 4 : 2);
+    double us = std::max(1.0, tiles * split / slots) * (kts * (f32 ? 2.0 : 1.45) * (0.6 + 0.4 * fill) + 6.0);
+    if (split > 1) us += 5.0 + 8.0 * split * (double)M * P / 4e6;
+    if (us < least) {
+      least = us;
+      best = split;
+    }
+  }
+  return best;
+}
+
+hipError_t launch_q4(const Q4Args& args, int act, hipStream_t s) {
+  Q4Args a = args;
+  // E = 1 with offsets: rows outside the group are not to be written, so no slices
+  const int split = q4_split(act, a.epi, a.l.M, a.l.N, (int)a.l.K, a.off == nullptr ? 1 : std::max(a.E, 2));
+  if (split == 0) return launch_q4_few(a, act, s);
+  a.l.split = split;
+  if (split == 1) a.l.part = nullptr;
+  return launch_q4_tile(a, act, s);
 }
 
 }  // namespace mok

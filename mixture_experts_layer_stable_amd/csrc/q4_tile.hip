@@ -45,11 +45,12 @@ __global__ __launch_bounds__(Tl::NT, sizeof(T) == 2 ? 2 : 1) void q4_tile_kernel
   constexpr int BNO = SW ? 64 : 128;  // outputs of a tile's columns
   const int NT = (a.N + BNO - 1) / BNO;
   GroupTile t;
-  int mt, nt;
+  int mt, nt, slice = 0;
   if (qa.off == nullptr) {
-    const int MT = (int)((a.M + Tl::BM - 1) / Tl::BM);
+    const int MT = (int)((a.M + Tl::BM - 1) / Tl::BM), L = xcd_logical(blockIdx.x, gridDim.x);
     t = {0, 0, (int)a.M, 0, MT};
-    band_walk(xcd_logical(blockIdx.x, gridDim.x), MT, NT, mt, nt);
+    slice = L / (MT * NT);
+    band_walk(L - slice * MT * NT, MT, NT, mt, nt);
   } else {
     GroupScan scan;
     scan.init(qa.off, qa.E, a.M, Tl::BM);
@@ -61,19 +62,22 @@ __global__ __launch_bounds__(Tl::NT, sizeof(T) == 2 ? 2 : 1) void q4_tile_kernel
   }
   const int64_t m0 = t.lo + (int64_t)mt * Tl::BM;
   const int n0 = nt * BNO, rows = (int)min<int64_t>(t.hi - m0, Tl::BM);
-  const uint32_t K = (uint32_t)a.K, KG = K / G;
+  // this slice of K: whole pieces of 128 from k0 on
+  const uint32_t KF = (uint32_t)a.K, pieces = (KF + 127) / 128;
+  const uint32_t k0 = (uint32_t)((uint64_t)pieces * slice / a.split) * 128;
+  const uint32_t K = min(KF, (uint32_t)((uint64_t)pieces * (slice + 1) / a.split) * 128) - k0, KG = K / G;
   // first output column of tile column j, and its row of w (columns past N re-read the last one)
   const auto col = [&](int j) { return SW ? n0 + (j / 64) * 32 + (j & 31) : n0 + j; };
   const auto wrow = [&](int j) { return t.g * P + min(col(j), a.N - 1) + (SW && (j & 32) ? a.N : 0); };
 
   const auto frow_a = [&](int f) { return wm * Tl::WTM + f * 32; };
   typename C::OA oa;
-  oa.init((const T*)a.a + m0 * K, 0, K, [&](int row) { return (uint32_t)min(row, rows - 1) * (uint32_t)(ES * K); }, frow_a,
-          wave, lane);
+  oa.init((const T*)a.a + m0 * KF + k0, 0, K, [&](int row) { return (uint32_t)min(row, rows - 1) * (uint32_t)(ES * KF); },
+          frow_a, wave, lane);
   // Raw loads of this lane: 16 bytes of codes of row tid / 2 (bf16: half tid % 2 of its K-tile; fp32: a row is 16
   // bytes, rows tid % 128); scale and zero point of row tid / 2 (group tid % 2 of the K-tile, if it has two).
-  const uint8_t* wq = (const uint8_t*)a.b + wrow(BF ? tid >> 1 : tid & 127) * (K / 2);
-  const uint64_t sg = (uint64_t)wrow(tid >> 1) * KG;
+  const uint8_t* wq = (const uint8_t*)a.b + wrow(BF ? tid >> 1 : tid & 127) * (KF / 2) + k0 / 2;
+  const uint64_t sg = (uint64_t)wrow(tid >> 1) * (KF / G) + k0 / G;
   const uint32_t lds = lds_offset(smem);
   const auto issue_raw = [&](uint32_t kt) {
     const uint32_t to = lds + C::R0 + kt % C::kRaw * C::RAW + wave * 1024;
@@ -174,7 +178,7 @@ __global__ __launch_bounds__(Tl::NT, sizeof(T) == 2 ? 2 : 1) void q4_tile_kernel
     uint32_t sr[2][2] = {{0, 0}, {0, 0}};  // [half of the K-tile][f]: scales as loaded, of the group that ends there
     uint32_t sh[2] = {0, 0};               // [f]: low bits of the index of column f's first scale
 #pragma unroll
-    for (int f = 0; f < 2; ++f) sh[f] = (uint32_t)wrow(wn * Tl::WTN + f * 32 + (lane & 31)) * KG;
+    for (int f = 0; f < 2; ++f) sh[f] = (uint32_t)wrow(wn * Tl::WTN + f * 32 + (lane & 31)) * (KF / G) + k0 / G;
     float s[2] = {0.0f, 0.0f};  // of the group that ended last
     const auto read_scales = [&](const char* raw, uint32_t (&to)[2][2]) {
 #pragma unroll
@@ -240,6 +244,7 @@ __global__ __launch_bounds__(Tl::NT, sizeof(T) == 2 ? 2 : 1) void q4_tile_kernel
                 const uint32_t wd = u == 0 ? w.x : (u == 1 ? w.y : (u == 2 ? w.z : w.w));
                 lo = wd & 0x0F0F0F0Fu;
                 hi = wd >> 4 & 0x0F0F0F0Fu;
+                asm("" : "+v"(lo), "+v"(hi));  // bytes: one conversion each
               }
               op[q] = bf16x2_rne((float)(lo >> (8 * q) & 0xFFu) - z, (float)(hi >> (8 * q) & 0xFFu) - z);
               if constexpr (q == 3)
@@ -309,7 +314,16 @@ __global__ __launch_bounds__(Tl::NT, sizeof(T) == 2 ? 2 : 1) void q4_tile_kernel
     for (int i = 0; i < LPR / 2; ++i) {
       const int row = lane / LPR + (64 / LPR) * i, c = (lane % LPR) * 8;
       const int mm = wm * Tl::WTM + m * 32 + row, cc = col(wn * Tl::WTN + c);
-      if (mm < rows && cc < a.N) {
+      if (mm < rows && cc < a.N && a.part != nullptr) {
+        float p[8];
+        float* to = a.part + ((int64_t)slice * a.M + m0 + mm) * P + cc;
+        load8(patch + row * kDensePatch + c, p);
+        store8(to, p);
+        if constexpr (SW) {
+          load8(patch + row * kDensePatch + 32 + c, p);
+          store8(to + a.N, p);
+        }
+      } else if (mm < rows && cc < a.N) {
         const Raw8<T> add = linear_add8<T>(a, m0 + mm, cc);
         float p[8], u[8];
         load8(patch + row * kDensePatch + c, p);
@@ -324,7 +338,7 @@ __global__ __launch_bounds__(Tl::NT, sizeof(T) == 2 ? 2 : 1) void q4_tile_kernel
 template <typename T, class Tl, bool SW>
 void run_tile(const Q4Args& a, hipStream_t s) {
   const int bno = SW ? 64 : 128;
-  const dim3 grid((unsigned)(q4_tiles_bound(a, Tl::BM) * ((a.l.N + bno - 1) / bno)));
+  const dim3 grid((unsigned)(q4_tiles_bound(a, Tl::BM) * ((a.l.N + bno - 1) / bno) * a.l.split));
   if (a.group == 32) hipLaunchKernelGGL((q4_tile_kernel<T, Tl, SW, 32>), grid, dim3(Tl::NT), 0, s, a);
   else if (a.group == 64) hipLaunchKernelGGL((q4_tile_kernel<T, Tl, SW, 64>), grid, dim3(Tl::NT), 0, s, a);
   else hipLaunchKernelGGL((q4_tile_kernel<T, Tl, SW, 128>), grid, dim3(Tl::NT), 0, s, a);
@@ -336,11 +350,23 @@ void run_tile(const Q4Args& a, hipStream_t s) {
   else run_tile<T, Tl, false>(a, s);
 }
 
+template <typename T>
+void run_join(const Q4Args& a, hipStream_t s) {
+  if (a.epi == MOK_EPI_SWIGLU) linear_join<LIN_FWD, MOK_EPI_SWIGLU, T, T>(a.l, s);
+  else if (a.epi == MOK_EPI_SILU) linear_join<LIN_FWD, MOK_EPI_SILU, T, T>(a.l, s);
+  else if (a.epi == MOK_EPI_GELU) linear_join<LIN_FWD, MOK_EPI_GELU, T, T>(a.l, s);
+  else linear_join<LIN_FWD, MOK_EPI_NONE, T, T>(a.l, s);
+}
+
 }  // namespace
 
-hipError_t launch_q4_tile(const Q4Args& a, int act, int bm, hipStream_t s) {
+hipError_t launch_q4_tile(const Q4Args& a, int act, hipStream_t s) {
   if (act == MOK_F32) run_tile<float, Tiling<128, 128, 2, 2>>(a, s);
   else run_tile<bf16, Tiling<128, 128, 2, 2>>(a, s);
+  if (a.l.split > 1) {
+    if (act == MOK_F32) run_join<float>(a, s);
+    else run_join<bf16>(a, s);
+  }
   return hipGetLastError();
 }
 

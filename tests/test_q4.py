@@ -46,8 +46,9 @@ class Case:
     def forward(self, bias=True, res=True):
         d, dev = self.d, lambda v: v.to(DEV)
         y = torch.full((d.M, d.N), KEEP, dtype=self.t, device=DEV)
+        ws = torch.full((max(self.mok.q4_workspace_query(d)["fwd_ws"], 16),), 255, dtype=torch.uint8, device=DEV)
         self.mok.q4_forward(d, dev(self.x), dev(self.q), dev(self.s), y, z=None if self.z is None else dev(self.z),
-                            off=self.goff, bias=dev(self.bias) if bias else None, res=dev(self.res) if res else None)
+                            off=self.goff, bias=dev(self.bias) if bias else None, res=dev(self.res) if res else None, ws=ws)
         return y
 
     def check(self, bias=True, res=True):
@@ -238,7 +239,8 @@ def test_in_place_captured_and_on_another_stream():
         dev = lambda v: v.to(DEV)
         want, same = c.forward(), dev(c.res).clone()
         x, q, s, z, b, r = (dev(v) for v in (c.x, c.q, c.s, c.z, c.bias, c.res))
-        c.mok.q4_forward(c.d, x, q, s, same, z=z, off=c.goff, bias=b, res=same)
+        ws = torch.empty(max(c.mok.q4_workspace_query(c.d)["fwd_ws"], 16), dtype=torch.uint8, device=DEV)
+        c.mok.q4_forward(c.d, x, q, s, same, z=z, off=c.goff, bias=b, res=same, ws=ws)
         assert torch.equal(want, same)
         st = torch.cuda.Stream()
         st.wait_stream(torch.cuda.current_stream())
@@ -249,11 +251,11 @@ def test_in_place_captured_and_on_another_stream():
         y = torch.empty_like(want)
         graph = torch.cuda.CUDAGraph()
         with torch.cuda.graph(graph):
-            c.mok.q4_forward(c.d, x, q, s, y, z=z, off=c.goff, bias=b, res=r)
+            c.mok.q4_forward(c.d, x, q, s, y, z=z, off=c.goff, bias=b, res=r, ws=ws)
         for _ in range(3):
             x.mul_(0.75)
             eager = torch.empty_like(y)
-            c.mok.q4_forward(c.d, x, q, s, eager, z=z, off=c.goff, bias=b, res=r)
+            c.mok.q4_forward(c.d, x, q, s, eager, z=z, off=c.goff, bias=b, res=r, ws=ws)
             y.fill_(KEEP)
             graph.replay()
             torch.cuda.synchronize()
