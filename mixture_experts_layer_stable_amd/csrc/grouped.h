@@ -87,8 +87,9 @@ struct GroupedArgs {
   const int32_t* off;  // [E + 1]
   int E;
 };
+constexpr int kShortTile = 6;
 struct GroupedPlan {
-  int tile;   // as LinearPlan's, or kFewTile, or kFewTile + 1 (32 rows)
+  int tile;   // as LinearPlan's, or kFewTile, kFewTile + 1 (32 rows), or LIN_DW's kShortTile
   int split;  // LIN_DW: slices of every group's rows
 };
 GroupedPlan grouped_plan(int kind, int act, int epi, int64_t M, int N, int64_t K, int E);

@@ -117,8 +117,9 @@ GroupedPlan grouped_plan(int kind, int act, int epi, int64_t M, int N, int64_t K
       tiles = bound = (double)((M + c.bm - 1) / c.bm) * (double)nt * E;
       kt = (double)all / E / (double)bk + 0.5;
     } else {
-      // a group's last tile is half full on average
-      tiles = std::max(groups, (double)M / c.bm + 0.5 * groups) * (double)nt;
+      // a group's last tile is half full on average (256 rows: an eighth of a tile is lost, see grouped_dense.h)
+      const bool cut = c.bm == 256;
+      tiles = std::max(groups * (cut ? 0.4 : 1.0), (double)M / c.bm + (cut ? 0.125 : 0.5) * groups) * (double)nt;
       bound = (double)group_tiles_bound(M, E, c.bm) * (double)nt;
       kt = (double)((K + bk - 1) / bk);
     }
@@ -140,6 +141,12 @@ GroupedPlan grouped_plan(int kind, int act, int epi, int64_t M, int N, int64_t K
         best = {t, split};
       }
     }
+  }
+  if (kind == LIN_DW && !f32) {
+    // K-tiles of 32 rows, two workgroups a CU, and what a tile takes besides them
+    const double tiles = (double)((M + 255) / 256) * (double)((N + 127) / 128) * E, kt = (double)all / E / 32 + 0.5;
+    const double us = std::max(1.0, tiles / 512) * (kt * 0.86 * (0.6 + 0.4 * std::min(1.0, tiles / 512)) + 5.7);
+    if (tiles < (1 << 24) && us < least) best = {kShortTile, 1};
   }
   if (kind == LIN_FWD) {
     for (int rt = 1; rt <= 2; ++rt) {
@@ -168,7 +175,7 @@ hipError_t launch_grouped(const GroupedArgs& args, int kind, int act, int epi, b
   GroupedArgs a = args;
   const GroupedPlan p = grouped_plan(kind, act, epi, a.l.M, a.l.N, a.l.K, a.E);
   a.l.split = p.split;
-  if (p.tile >= kFewTile) return launch_grouped_few(a, p.tile - kFewTile + 1, act, epi, s);
+  if (p.tile == kFewTile || p.tile == kFewTile + 1) return launch_grouped_few(a, p.tile - kFewTile + 1, act, epi, s);
   if (act == MOK_BF16) return launch_grouped_bf16(a, p.tile, kind, epi, out_f32, s);
   return launch_grouped_f32(a, p.tile, kind, epi, s);
 }

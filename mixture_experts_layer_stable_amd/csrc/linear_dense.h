@@ -89,10 +89,10 @@ struct DenseK {
 // MN-contiguous operand: k-row k of the tile starts at sbase + k * ld bytes; KR k-rows of ROWS
 // elements per stage. Rows at or past K read zeros, 16-byte column chunks at or past `cols` read the
 // row's first chunk (their results are not stored).
-template <typename T, int ROWS, int NF, int NW>
+template <typename T, int ROWS, int NF, int NW, int KR_ = kRowBytes / (int)sizeof(T)>
 struct DenseMN {
   static constexpr bool F32 = std::is_same<T, float>::value;
-  static constexpr int KR = kRowBytes / (int)sizeof(T), VE = Elem<T>::VE;
+  static constexpr int KR = KR_, VE = Elem<T>::VE;
   static constexpr int PITCH = ROWS * (int)sizeof(T);
   static constexpr int BYTES = KR * PITCH;
   static constexpr int NI = BYTES / (1024 * NW);
@@ -147,7 +147,7 @@ struct DenseMN {
     }
   }
   __device__ __forceinline__ uint4 frag(const char* stage, int f, int ks) const {
-    const char* a = stage + foff[f] + ks * (KR / 4) * PITCH;
+    const char* a = stage + foff[f] + ks * (F32 ? 8 : 16) * PITCH;
     if constexpr (F32) {
       const auto at = [&](int k) { return *reinterpret_cast<const uint32_t*>(a + k * PITCH); };
       return make_uint4(at(0), at(1), at(2), at(3));
@@ -343,14 +343,13 @@ __device__ __forceinline__ void band_walk(int r, int MT, int NT, int& mt, int& n
 
 // One workgroup's tile at row m0, column n0, over K-tiles kt0 .. kt1-1; rows end at a.M. part: nullptr, or
 // where a slice's sums go (linear_join_kernel adds the slices).
-template <typename T, class Tl, int KIND, int EPI, typename TO, bool PART>
+// NTS: 256 x 256 tiles belong to outputs that no cache keeps: stored past L2, they leave it to the
+// operands' bands (16384 x (2 x 2048) x 7168: 818 -> 745 us).
+template <typename T, class Tl, int KIND, int EPI, typename TO, bool PART, bool NTS = (Tl::BM * Tl::BN >= 256 * 256)>
 __device__ __forceinline__ void dense_work(const LinearArgs& a, int64_t m0, int n0, int64_t kt0, int64_t kt1, float* part,
                                            char* smem) {
   using Cfg = DenseCfg<T, Tl, KIND, EPI>;
   constexpr bool SW = Cfg::SW;
-  // 256 x 256 tiles belong to outputs that no cache keeps: stored past L2, they leave it to the
-  // operands' bands (16384 x (2 x 2048) x 7168: 818 -> 745 us)
-  constexpr bool NTS = Tl::BM * Tl::BN >= 256 * 256;
   constexpr int64_t ES = sizeof(T);
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wm = wave / Tl::WN, wn = wave % Tl::WN;
