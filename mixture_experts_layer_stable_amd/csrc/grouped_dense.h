@@ -162,20 +162,22 @@ __global__ __launch_bounds__(Tl::NT) void grouped_dense_kernel(GroupedArgs ga) {
     const int L = xcd_logical(blockIdx.x, tiles);
     const GroupTile t = scan.find(L / NT, Tl::BM);
     band_walk(L - t.first * NT, t.tiles, NT, mt, nt);
-    a.M = t.hi;  // rows of other groups are neither read nor written
     a.b = (const T*)a.b + (int64_t)t.g * (KIND == LIN_FWD ? P * a.K : a.K * a.N);
     if (KIND == LIN_FWD && a.bias != nullptr) a.bias += t.g * P;
-    const int64_t KT = (a.K + Cfg::BKE - 1) / Cfg::BKE, m0 = t.lo + (int64_t)mt * Tl::BM;
-    // 256 x 256 tiles: a group's last one is as high as its rows need (64, 128, 192 or 256), which costs an eighth
-    // of a tile a group where whole tiles cost half of one
+    // 256 x 256 tiles: a group's rows are shared out evenly, and its tiles are as high as that needs (64, 128, 192 or
+    // 256): they run side by side at one pace and take w from L2. Where a group's last tile alone was lower it ran
+    // ahead, and w came from HBM once for each (320 rows a group, 48 of 4096 x 7168: 1063 us).
     constexpr bool CUT = Tl::BM == 256;
+    const int64_t KT = (a.K + Cfg::BKE - 1) / Cfg::BKE;
+    const int high = CUT ? (t.hi - t.lo + t.tiles - 1) / t.tiles : Tl::BM;
+    const int64_t m0 = t.lo + (int64_t)mt * high, left = min((int64_t)t.hi, m0 + high) - m0;
+    a.M = m0 + left;  // rows of other groups are neither read nor written
     using H1 = Tiling<CUT ? 64 : Tl::BM, Tl::BN, Tl::WM, Tl::WN>;
     using H2 = Tiling<CUT ? 128 : Tl::BM, Tl::BN, Tl::WM, Tl::WN>;
     using H3 = Tiling<CUT ? 192 : Tl::BM, Tl::BN, Tl::WM, Tl::WN>;
-    const int64_t left = t.hi - m0;
-    if (!CUT || left > 192) dense_work<T, Tl, KIND, EPI, TO, false>(a, m0, nt * Cfg::BN, 0, KT, nullptr, smem);
-    else if (left > 128) dense_work<T, H3, KIND, EPI, TO, false, true>(a, m0, nt * Cfg::BN, 0, KT, nullptr, smem);
-    else if (left > 64) dense_work<T, H2, KIND, EPI, TO, false, true>(a, m0, nt * Cfg::BN, 0, KT, nullptr, smem);
+    if (!CUT || high > 192) dense_work<T, Tl, KIND, EPI, TO, false>(a, m0, nt * Cfg::BN, 0, KT, nullptr, smem);
+    else if (high > 128) dense_work<T, H3, KIND, EPI, TO, false, true>(a, m0, nt * Cfg::BN, 0, KT, nullptr, smem);
+    else if (high > 64) dense_work<T, H2, KIND, EPI, TO, false, true>(a, m0, nt * Cfg::BN, 0, KT, nullptr, smem);
     else dense_work<T, H1, KIND, EPI, TO, false, true>(a, m0, nt * Cfg::BN, 0, KT, nullptr, smem);
   }
 }
