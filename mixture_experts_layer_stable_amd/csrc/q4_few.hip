@@ -91,11 +91,11 @@ __global__ __launch_bounds__(64 * kWaves) void q4_few_kernel(Q4Args qa) {
       if (begin) {
         const int all = total * NS, wgs = min(all, (int)gridDim.x);
         if ((int)blockIdx.x >= wgs) return;
-        const int l = xcd_logical(blockIdx.x, wgs), share = all / wgs, more = all - share * wgs;
+        const int l = xcd_logical(blockIdx.x, wgs), share = all == wgs ? 1 : all / wgs, more = all - share * wgs;
         cur = l * share + min(l, more);
         end = cur + share + (l < more);
       }
-      q = cur / NS;
+      q = total == 1 ? 0 : cur / NS;  // (a division takes 0.1 us of a small call)
       t = {0, 0, (int)a.M, 0, total};
       if (qa.off != nullptr) t = scan.find(q, kRows);
     }
@@ -113,24 +113,28 @@ __global__ __launch_bounds__(64 * kWaves) void q4_few_kernel(Q4Args qa) {
     while ((1u << mb) < M) ++mb;
     const uint32_t pb = (16 * 16 * XV) << mb;  // bytes of a piece
     const bool staged = pieces * pb > XB;
-    const uint32_t XR = staged ? XB / 2 / pb / WS : rounds, SP = staged ? XR * WS : pieces;  // rounds, pieces of a stage
+    uint32_t XR = rounds, SP = pieces, stages = 1;  // rounds and pieces of a stage, stages
+    if (staged) {
+      XR = XB / 2 / pb / WS;
+      SP = XR * WS;
+      stages = (pieces + SP - 1) / SP;
+    }
     const auto slot = [&](uint32_t p, uint32_t step, uint32_t h, uint32_t lg, uint32_t m) {  // of 16 bytes
       return ((((p * 4 + step) * XV + h) * 4 + lg) << mb) + ((m ^ (4 * lg + step)) & ((1u << mb) - 1));
     };
     // 64 vectors of a row of the pieces from p0 on: block i of M * nb, nb blocks a row
     const auto get_x = [&](uint32_t p0, uint32_t i, uint32_t nb) {
-      const uint32_t m = i / nb, c = (i - m * nb) * 64 + lane, k = p0 * kPiece + c * (8 / XV);
+      const uint32_t m = M == 1 ? 0 : i / nb, c = (i - m * nb) * 64 + lane, k = p0 * kPiece + c * (8 / XV);
       const uint4 d = ldg16(x + (uint64_t)min(m, M - 1) * K + min(k, K - 8 / XV));
       return k < K ? d : make_uint4(0, 0, 0, 0);
     };
     const auto put_x = [&](char* to, uint32_t i, uint32_t nb, uint32_t n, uint4 d) {
-      const uint32_t m = i / nb, c = (i - m * nb) * 64 + lane, u = c / XV % 16, h = c % XV;
+      const uint32_t m = M == 1 ? 0 : i / nb, c = (i - m * nb) * 64 + lane, u = c / XV % 16, h = c % XV;
       if constexpr (BF) d = order_bf16(d);
       if (m < M && c < n)
         *reinterpret_cast<uint4*>(to + 16 * slot(c / (16 * XV), GP > 1 ? u / 4 : u % 4, h, GP > 1 ? u % 4 : u / 4, m)) = d;
     };
     const uint32_t sv = SP * (16 * XV), sb = (sv + 63) / 64;  // vectors and blocks of a row of a stage
-    const uint32_t stages = (pieces + SP - 1) / SP;
     uint4 xr[NX];
     const auto load_x = [&](uint32_t st) {
 #pragma unroll
