@@ -643,8 +643,8 @@ typedef struct mok_q4_desc {
 mok_status mok_q4_workspace_query(const mok_q4_desc* d, size_t* fwd_ws);
 
 /*
- * mok_q4_quantize -- codes, scales and (z not NULL) zero points of finite w [E][P][K] in act. For the values v
- * of a group, in fp32, each division and rint (ties to even) rounded:
+ * mok_q4_quantize -- codes, scales and (z not NULL) zero points of finite w [E][P][K] in act (hi - lo finite too).
+ * For the values v of a group, in fp32, each division and rint (ties to even) rounded:
  *   z NULL:  s = max|v| / 7 rounded to act,  code = clamp(rint(v / s) + 8, 0, 15)
  *   else:    lo = min(v, 0), hi = max(v, 0) over the group,  s = (hi - lo) / 15 rounded to act,
  *            z = clamp(rint(-lo / s), 0, 15),  code = clamp(rint(v / s) + z, 0, 15)
@@ -657,6 +657,8 @@ mok_status mok_q4_quantize(const mok_q4_desc* d, const void* w, void* q, void* s
  * mok_q4_forward -- p = x_r w[e]^T + bias[e];  y_r = f(p) + res_r, in fp32, rounded once; w enters as the exact
  * values of its codes and scales.  off as of mok_grouped_desc; NULL (E = 1 only): one group of all M rows.
  * x [M][K], bias [E][P] fp32 or NULL, res [M][N] or NULL (may be the same array as y), y [M][N].
+ * Up to some dozens of rows a group, bf16 x is multiplied by 16 + code and by 16 + z, whose difference is
+ * exact but for fp32's sums: an infinity in x gives NaN there, and sums of 32 |x| have to stay below 3.4e38.
  */
 mok_status mok_q4_forward(const mok_q4_desc* d, const void* x, const void* q, const void* s, const uint8_t* z,
                           const float* bias, const int32_t* off, const void* res, void* y, void* ws, size_t ws_bytes,

@@ -24,14 +24,17 @@ __global__ __launch_bounds__(256) void grouped_dpre_kernel(const T* __restrict__
   m = max(m, (int)blockIdx.y * rows);
   const int end = (int)min<int64_t>(((int64_t)blockIdx.y + 1) * rows, group_clamp(off[E], 0, M));
   while (m < end) {
-    int g = 0, hi = E;  // the last group that begins at or before row m
-    while (hi - g > 1) {
-      const int mid = (g + hi) / 2;
-      if (off[mid] <= m) g = mid;
-      else hi = mid;
+    int g = 0, m1 = end;
+    if (part != nullptr) {  // the sums end with the group
+      int hi = E;  // the last group that begins at or before row m
+      while (hi - g > 1) {
+        const int mid = (g + hi) / 2;
+        if (off[mid] <= m) g = mid;
+        else hi = mid;
+      }
+      m1 = min(end, off[g + 1]);
+      if (m1 <= m) return;  // offsets that descend
     }
-    const int m1 = min(end, off[g + 1]);
-    if (m1 <= m) return;  // offsets that descend
     float sg[8], su[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) sg[i] = su[i] = 0.0f;

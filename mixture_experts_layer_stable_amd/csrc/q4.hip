@@ -74,7 +74,7 @@ hipError_t launch_q4_quantize(const void* w, int64_t rows, int K, int group, int
 }
 
 // The faster of the two kernels by estimates (us) fitted to shapes from 1 to 4096 rows. q4_few.hip: what 16 rows
-// of a group take for a million codes. Tiles: K-tiles (of 64, fp32 32) one after the other, half as long on
+// of a group take for a million codes (up to 2^27 rows, whose tiles GroupScan counts). Tiles: K-tiles (of 64, fp32 32) one after the other, half as long on
 // an empty chip as on a full one, in rounds of 512 (fp32 256); slices of K, of a dense product only (a second
 // launch that adds them would have to know the rows' groups), cost their partial products' way to memory and back.
 int q4_split(int act, int epi, int64_t M, int N, int K, int E) {
@@ -82,7 +82,7 @@ int q4_split(int act, int epi, int64_t M, int N, int K, int E) {
   const bool f32 = act == MOK_F32;
   const double P = epi == MOK_EPI_SWIGLU ? 2.0 * N : N, groups = (double)std::min<int64_t>(E, M);
   const double row_tiles = std::max(groups, (double)M / 16 + 0.5 * groups), rows = (double)M / groups;
-  double least = 6.0 + row_tiles * P * K * 1e-6 * (f32 ? 0.75 : (rows > 4 ? 0.38 : 0.2));
+  double least = M > (1 << 27) ? 1e30 : 6.0 + row_tiles * P * K * 1e-6 * (f32 ? 0.75 : (rows > 4 ? 0.38 : 0.2));
   int best = 0;
   const double tiles = std::max(groups, (double)M / 128 + 0.5 * groups) * std::max(1.0, P / 128), slots = f32 ? 256 : 512;
   const int pieces = (K + 127) / 128;

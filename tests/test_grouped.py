@@ -146,6 +146,17 @@ def test_larger(counts, N, K):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("N,K,epi", [(2048, 1024, "none"), (1024, 2048, "silu"), (1032, 1032, "swiglu")])
+def test_tiles_as_high_as_their_groups(N, K, epi):
+    """Groups of one row up to a few tiles, at both sides of every height that a tile of 256 rows is cut to."""
+    counts = [1, 63, 64, 65, 127, 128, 129, 0, 191, 192, 193, 255, 256, 257, 320, 384, 385, 511, 512, 513, 700, 769, 20, 300]
+    print("case grouped heights", N, K, epi, flush=True)
+    c = Case(counts, N, K, "bf16", epi, lead=1, tail=4)
+    c.check_forward(res=epi == "none")
+    c.check_backward(add=epi == "none")
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("E", [63, 64, 65, 1000, 1024])
 def test_many_groups(E):
     """A lane of the search holds one group, or up to 16; runs of empty ones."""

@@ -113,6 +113,43 @@ def test_many_rows(M, N, K, G):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("counts,N,K,G", [([1, 3, 0, 16] * 40, 520, 256, 128),    # a tile of w a wave
+                                          ([2, 1, 0, 5] * 12, 520, 288, 32),       # two waves a tile
+                                          ([16, 9, 1] * 8, 776, 4352, 64),         # two waves, x in stages
+                                          ([16, 12] * 34, 968, 4352, 128),         # one wave, x in stages
+                                          ([20, 40, 3, 0, 17], 136, 1088, 64)])    # groups of more than 16 rows
+def test_few_rows_of_many_groups(counts, N, K, G):
+    for act, epi in (("bf16", "swiglu"), ("f32", "none")) if K < 2000 else (("bf16", "none"),):
+        print("case q4 many groups", len(counts), sum(counts), N, K, G, act, epi, flush=True)
+        Case(counts, N, K, G, act, epi, zeros=True, tail=2).check(bias=False)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("G", [32, 64, 128])
+def test_tiles_of_ragged_groups(G):
+    for epi in ("none", "swiglu"):
+        print("case q4 tiles", G, epi, flush=True)
+        Case([700, 3, 0, 900, 129], 1032, 1920 if G == 128 else 2016 // G * G, G, "bf16", epi, zeros=epi == "none", lead=3, tail=5).check()
+
+
+@pytest.mark.gpu
+def test_infinite_weights_and_rows():
+    """An infinite scale reaches its group of rows of w only, a row of x that is not finite its row of y only."""
+    for M in (5, 600):
+        c = Case(M, 72, 256, 64, "bf16", "none", True)
+        clean = c.forward(bias=False, res=False).cpu()
+        c.s[0, 7, 1] = float("inf")
+        c.x[3, 100] = float("inf")
+        c.x[4, 0] = float("nan")
+        got = c.forward(bias=False, res=False).cpu()
+        keep = torch.ones_like(got, dtype=torch.bool)
+        keep[3:5] = False
+        keep[:, 7] = False
+        assert torch.equal(got[keep], clean[keep])
+        assert not torch.isfinite(got[:, 7]).any() and torch.isnan(got[4]).all()
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("group", [32, 64, 128])
 def test_every_code_and_zero_point_alone(group):
     """x = one unit vector: y is s (code - z) exactly (bf16: |code - z| s has at most 12 bits, rounded once)."""
