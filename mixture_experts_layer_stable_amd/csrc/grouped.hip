@@ -11,27 +11,26 @@ namespace {
 
 // ---- dp = dy f'(pre) of the rows in groups, and the bias gradient ----
 // As linear_dpre_kernel (a thread keeps eight columns and walks down the rows of a chunk, HBM-bound),
-// and at a group's last row the sums go out and start again. Empty groups are passed by a search.
+// and at a group's last row the sums go out and start again. A wave finds the group of a row in one round of
+// loads (a search by halves is a chain of them).
 template <typename T, int EPI>
 __global__ __launch_bounds__(256) void grouped_dpre_kernel(const T* __restrict__ dy, const T* __restrict__ pre,
                                                            const int32_t* __restrict__ off, int M, int N, int E, int rows,
                                                            T* __restrict__ dp, float* __restrict__ part) {
   constexpr bool SW = EPI == MOK_EPI_SWIGLU;
-  const int c = (blockIdx.x * 256 + threadIdx.x) * 8;
   const int64_t P = SW ? 2 * (int64_t)N : N;
-  if (c >= N) return;
+  const int c0 = (blockIdx.x * 256 + threadIdx.x) * 8, c = min(c0, N - 8);  // whole waves search
+  const bool live = c0 < N;
   int m = group_clamp(off[0], 0, M);
   m = max(m, (int)blockIdx.y * rows);
   const int end = (int)min<int64_t>(((int64_t)blockIdx.y + 1) * rows, group_clamp(off[E], 0, M));
   while (m < end) {
     int g = 0, m1 = end;
-    if (part != nullptr) {  // the sums end with the group
-      int hi = E;  // the last group that begins at or before row m
-      while (hi - g > 1) {
-        const int mid = (g + hi) / 2;
-        if (off[mid] <= m) g = mid;
-        else hi = mid;
-      }
+    if (part != nullptr) {  // the sums end with the group: the last one that begins at or before row m
+      int n = 0;
+#pragma unroll 4
+      for (int i = threadIdx.x & 63; i < ((E + 63) & ~63); i += 64) n += __popcll(__ballot(i < E && off[min(i, E)] <= m));
+      g = max(n - 1, 0);
       m1 = min(end, off[g + 1]);
       if (m1 <= m) return;  // offsets that descend
     }
@@ -51,11 +50,12 @@ __global__ __launch_bounds__(256) void grouped_dpre_kernel(const T* __restrict__
         if constexpr (SW) su[i] += u[i];
       }
       if constexpr (EPI != MOK_EPI_NONE) {
+        if (!live) continue;
         store8(dp + m * P + c, d);
         if constexpr (SW) store8(dp + m * P + N + c, u);
       }
     }
-    if (part == nullptr) continue;
+    if (part == nullptr || !live) continue;
     float* o = part + ((int64_t)blockIdx.y + g) * P + c;
     store8(o, sg);
     if constexpr (SW) store8(o + N, su);
