@@ -98,7 +98,7 @@ void run_dpre(const void* dy, const void* pre, const int32_t* off, int64_t M, in
 // The tile of least estimated time, as linear_plan's, for rows spread evenly over the groups: the
 // offsets stay on the device, and a launch's sizes and order of sums depend on the shape alone. Over 15 shapes
 // from 16 to 32768 rows of 2 to 151 groups, forward and dx, at every tile: the one taken is the fastest or
-// within a fifth of it (128 rows of 32 groups, 1024 x 1024: within a third before the few-row kernel's cost was set).
+// within a fifth of it.
 GroupedPlan grouped_plan(int kind, int act, int epi, int64_t M, int N, int64_t K, int E) {
   GroupedPlan best{0, 1};
   const int64_t all = kind == LIN_DW ? K : M;  // rows of all groups

@@ -18,7 +18,7 @@ __device__ __forceinline__ void put_row(void* p, const uint4& v) {
 }
 
 // out[r] = in[perm[r] / k], zeros for no slot. 2^lanes lanes copy a row, four vectors of it in flight. 16384 x 8
-// x 7168: 529 us (stores through the caches 564), 4.0 TB/s of each x read once: the experts' order reads every
+// x 7168: 489 us (529 on another card, where stores through the caches took 564), 4.0 TB/s of each x read once: the experts' order reads every
 // row of x eight times, far apart, and x (235 MB) does not stay in the last cache beside what is written.
 template <bool NT>
 __global__ __launch_bounds__(256) void dispatch_kernel(PermuteArgs a, int row_vecs, int lanes) {

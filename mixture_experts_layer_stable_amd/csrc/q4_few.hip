@@ -2,12 +2,16 @@
 //
 //   p[m][n] = sum over groups j of K of s[n][j] (sum_k x[m][k] (16 + q[n][k]) - (16 + z[n][j]) sum_k x[m][k])
 //
-// What bounds them is the codes' way from HBM, its latency, and next the instructions that a code takes. A
+// What bounds them is, from some hundred MB of codes on, the instructions that a code takes (128 rows of 48
+// groups, 7168 x 2048: 85 us, 3.6 TB/s; 2 x 2048 x 7168 each: 143 us, 4.1 TB/s), and in small calls the
+// latency of each step, of which the loop is less than half (one row, 2 x 2048 x 7168: 9.6 us). A
 // wave takes 16 rows of w (8 gate and 8 up rows for SWIGLU) and 128 codes of each at a time; four such
 // pieces are on their way while the four before them are worked on. Of a workgroup's eight waves WS share
-// a row tile, each a part of K, and 8 / WS tiles lie side by side. The workgroups, two a CU, share the tiles
+// a row tile, each a part of K, and 8 / WS tiles lie side by side. The workgroups, one a CU, share the tiles
 // of all groups evenly; a workgroup's rows of x stay in LDS for all of its tiles (or pass through it in two
 // stages), in the order in which the matrix units want them, so a wave streams codes from tile to tile.
+// (One workgroup for each set of tiles: 547 us for the 85. Codes through LDS by direct loads, or four pieces
+// in a ring of registers: not faster. Sixteen waves: slower, they spill.)
 // A code becomes a matrix operand without arithmetic: 16 + q in bf16 is 0x4180 | q << 3, two of a dword at
 // a time. A second multiplication, by -(16 + z), takes off what the offset brought in; both are exact in
 // fp32 up to its sums, and a group's result takes its scale in fp32. So w is never rounded to bf16.
@@ -136,11 +140,11 @@ __global__ __launch_bounds__(64 * kWaves) void q4_few_kernel(Q4Args qa) {
     };
     const uint32_t sv = SP * (16 * XV), sb = (sv + 63) / 64;  // vectors and blocks of a row of a stage
     uint4 xr[NX];
-    const auto load_x = [&](uint32_t st) {
+    const auto load_x = [&](uint32_t st) __attribute__((always_inline)) {
 #pragma unroll
       for (int i = 0; i < NX; ++i) xr[i] = get_x(st * SP, i * kWaves + wave, sb);
     };
-    const auto store_x = [&](uint32_t buf) {
+    const auto store_x = [&](uint32_t buf) __attribute__((always_inline)) {
 #pragma unroll
       for (int i = 0; i < NX; ++i) put_x(lds.x + (buf & 1) * (XB / 2), i * kWaves + wave, sb, sv, xr[i]);
     };
@@ -170,7 +174,7 @@ __global__ __launch_bounds__(64 * kWaves) void q4_few_kernel(Q4Args qa) {
       wz = qa.z + wr * KG;
     };
     const int last = set0 + nset - 1;
-    const auto load = [&](Batch& d) {
+    const auto load = [&](Batch& d) __attribute__((always_inline)) {
 #pragma unroll
       for (int n = 0; n < kBatch; ++n) {
         const uint32_t p = min((round_l + n) * WS + ks, pieces - 1);
@@ -194,7 +198,10 @@ __global__ __launch_bounds__(64 * kWaves) void q4_few_kernel(Q4Args qa) {
     f32x4_t acc = {0.0f, 0.0f, 0.0f, 0.0f};
     int set = set0;
     uint32_t round = 0, sc = 0, buf_round = 0;  // of the work; stages gone by; round within the stage
-    const auto work = [&](const Batch& d) {
+    // stagedc: whether x comes in stages, known to the compiler so that the rounds of a batch stay in one block
+    // and overlap
+    const auto work = [&](auto stagedc, const Batch& d) __attribute__((always_inline)) {
+      constexpr bool staged = decltype(stagedc)::value;
       float ds[GP];
       uint32_t dz[GP];
 #pragma unroll
@@ -204,9 +211,9 @@ __global__ __launch_bounds__(64 * kWaves) void q4_few_kernel(Q4Args qa) {
         if constexpr (BF) dz[j] = 0xC180C180u | (qa.zeros ? d.z[j] & 15u : 8u) * 0x00080008u;
         else dz[j] = __float_as_uint(qa.zeros ? (float)d.z[j] : 8.0f);
       }
-      static_for<0, kBatch>([&](auto nc) {
+      static_for<0, kBatch>([&](auto nc) __attribute__((always_inline)) {
         constexpr int n = decltype(nc)::value;
-        if (staged) {
+        if constexpr (staged) {
           if (buf_round == XR && round + n < rounds) {  // the next stage of x
             ++sc;
             store_x(sc);
@@ -224,12 +231,12 @@ __global__ __launch_bounds__(64 * kWaves) void q4_few_kernel(Q4Args qa) {
         for (int j = 0; j < GP; ++j) {
           const float s = __shfl(ds[j], r + 16 * n);
           const uint32_t z = __shfl(dz[j], r + 16 * n);
-          f32x4_t dd = {0.0f, 0.0f, 0.0f, 0.0f};
+          f32x4_t dd = {0.0f, 0.0f, 0.0f, 0.0f}, oo = dd;
 #pragma unroll
           for (int e = j * (4 / GP); e < (j + 1) * (4 / GP); ++e) {
             const uint4 xv = *reinterpret_cast<const uint4*>(xs + xoff[e]);
             if constexpr (BF) {
-              dd = mma16<bf16>(xv, make_uint4(z, z, z, z), dd);
+              oo = mma16<bf16>(xv, make_uint4(z, z, z, z), oo);
               dd = mma16<bf16>(xv, codes_bf16(w[e]), dd);
             } else {
               const uint4 xw = *reinterpret_cast<const uint4*>(xs + xhalf + xoff[e]);
@@ -243,7 +250,7 @@ __global__ __launch_bounds__(64 * kWaves) void q4_few_kernel(Q4Args qa) {
             }
           }
 #pragma unroll
-          for (int c = 0; c < 4; ++c) acc[c] = __builtin_fmaf(s, dd[c], acc[c]);
+          for (int c = 0; c < 4; ++c) acc[c] = __builtin_fmaf(s, BF ? dd[c] + oo[c] : dd[c], acc[c]);
         }
       });
       round += kBatch;
@@ -283,7 +290,7 @@ __global__ __launch_bounds__(64 * kWaves) void q4_few_kernel(Q4Args qa) {
       else __builtin_amdgcn_wave_barrier();
       round = 0;
       ++set;
-      if (staged) buf_round = XR;  // the next set begins with the first stage
+      if constexpr (staged) buf_round = XR;  // the next set begins with the first stage
     };
 
     Batch b0, b1;
@@ -299,14 +306,18 @@ __global__ __launch_bounds__(64 * kWaves) void q4_few_kernel(Q4Args qa) {
       for (uint32_t i = wave; i < M * sb; i += kWaves) put_x(lds.x, i, sb, sv, get_x(0, i, sb));
     }
     lds_barrier();
-    while (true) {
-      load(b1);
-      work(b0);
-      if (set > last) break;
-      load(b0);
-      work(b1);
-      if (set > last) break;
-    }
+    const auto stream = [&](auto stagedc) __attribute__((always_inline)) {
+      while (true) {
+        load(b1);
+        work(stagedc, b0);
+        if (set > last) break;
+        load(b0);
+        work(stagedc, b1);
+        if (set > last) break;
+      }
+    };
+    if (staged) stream(std::true_type());
+    else stream(std::false_type());
   }
 }
 
