@@ -6,8 +6,8 @@
 // exact in bf16, and the sums of each K-tile (of each group of 32, where a scale ends inside it) take their
 // scale in fp32, so w is never rounded. fp32: the operand is s (q - z), rounded once.
 // What bounds it is vector instructions beside the MFMAs: the codes' conversion, which every row tile
-// does again, and the sums' scaling. 4096 rows, 2 x 2048 x 7168: 333 us (720 TFLOP/s); 7168 x 2048: 192, in groups of 32
-// 307 (twice the scalings, and some registers spill). The sums are as many registers again as the
+// does again, and the sums' scaling. 4096 rows, 2 x 2048 x 7168: 322 us (747 TFLOP/s); 7168 x 2048: 169, in groups of 32
+// 189 (twice the scalings; with last K-tiles that branched around their loads, and spilled, 192 and 307). The sums are as many registers again as the
 // accumulators: 256 x 128 tiles spill (387 for the 333), 128 x 128 with one workgroup a CU take 0.79 us
 // a K-tile where two take 1.45 for both. fp32, 4096 rows, 2048 x 2048: 311 us (110 TFLOP/s).
 // Few tiles of a dense product take slices of K, joined by linear_join (128 rows, 2 x 2048 x 7168: 101 -> 36 us).
@@ -198,8 +198,19 @@ __global__ __launch_bounds__(Tl::NT, sizeof(T) == 2 ? 2 : 1) void q4_tile_kernel
 #pragma unroll
       for (int r = 0; r < 16; ++r) acc[m][f][r] = __builtin_fmaf(s[f], grp[m][f][r], acc[m][f][r]);
     };
-    const auto step = [&](auto fullc, uint32_t kt) {
-      constexpr bool FULL = decltype(fullc)::value;
+    const auto scale = [&](uint32_t kt, int half) {
+#pragma unroll
+      for (int f = 0; f < 2; ++f) {
+        const uint32_t ix = sh[f] + kt * BK / G + half;
+        s[f] = __uint_as_float(sr[half][f] >> ((ix & 1) * 16) << 16);
+      }
+    };
+    // The step's loads have no branch, around which the sums would be spilled: past the end they take the last K-tile
+    // again, and the second half of half a K-tile (G = 32) is the first one once more, which no one reads.
+    const auto upper = [&](int j) { return ((lane & 7) ^ swz_k(8 * (wave + Tl::NW * j) + (lane >> 3))) >> 2 & 1; };
+    static_assert(Tl::NW == 4, "upper(j) goes by j % 2");
+    const uint32_t odd = G == 32 && KT * BK != K ? 64 : 0, hs[2] = {odd * upper(0), odd * upper(1)};
+    const auto step = [&](uint32_t kt) {
       const uint32_t nk = kt + 1;
       const char* raw = smem + C::R0 + nk % C::kRaw * C::RAW;
       char* to = smem + C::B0 + (nk & 1) * (C::BN * 128) + brow * 128;
@@ -258,13 +269,7 @@ __global__ __launch_bounds__(Tl::NT, sizeof(T) == 2 ? 2 : 1) void q4_tile_kernel
           }
           // scales of the groups that end in the next K-tile; of the group that has just ended
           if constexpr (slot == NM) read_scales(raw, srn);
-          if constexpr (i == NM - 1 && (ks == 3 || (G == 32 && ks == 1))) {
-#pragma unroll
-            for (int ff = 0; ff < 2; ++ff) {
-              const uint32_t ix = sh[ff] + min(kt * BK / G + (G == 32 && ks == 3 ? 1 : 0), KG - 1);
-              s[ff] = __uint_as_float(sr[G == 32 && ks == 3][ff] >> ((ix & 1) * 16) << 16);
-            }
-          }
+          if constexpr (i == NM - 1 && (ks == 3 || (G == 32 && ks == 1))) scale(kt, G == 32 && ks == 3);
           if constexpr (slot == 4 * NM - 1) {
 #pragma unroll
             for (int h = 0; h < (G == 32 ? 2 : 1); ++h)
@@ -273,7 +278,11 @@ __global__ __launch_bounds__(Tl::NT, sizeof(T) == 2 ? 2 : 1) void q4_tile_kernel
           }
           if constexpr (ks == 3) {
             constexpr int NI = C::OA::NI;
-            oa.template issue<FULL>(FULL ? kd : min(kd, KT - 1), dst, wave, i * NI / NM, (i + 1) * NI / NM);
+            const uint32_t kl = min(kd, KT - 1), end = G == 32 && kl == KT - 1 ? ~0u : 0u;
+            static_for<i * NI / NM, (i + 1) * NI / NM>([&](auto jc) {
+              constexpr int j = decltype(jc)::value;
+              load_lds_sv<16>(uniform_ptr(oa.base(kl, j, wave)), oa.voff[j] - (hs[j & 1] & end), dst + (wave + Tl::NW * j) * 1024);
+            });
             if constexpr (i == NM - 1) issue_raw(kt + 3);
           }
           __builtin_amdgcn_sched_barrier(0);
@@ -294,11 +303,21 @@ __global__ __launch_bounds__(Tl::NT, sizeof(T) == 2 ? 2 : 1) void q4_tile_kernel
     for (int m = 0; m < Tl::FM; ++m) fa[0][m] = oa.frag(smem, m, 0);
 #pragma unroll
     for (int f = 0; f < 2; ++f) fb[0][f] = *reinterpret_cast<const uint4*>(smem + C::B0 + foff[f][0]);
-    uint32_t kt = 0;
-    for (const uint32_t full = (uint32_t)oa.full(); kt + 2 < full; ++kt) step(std::true_type(), kt);
-#pragma unroll 1
-    for (; kt < KT; ++kt) step(std::false_type(), kt);
+    for (uint32_t kt = 0; kt < K / BK; ++kt) step(kt);
     static_for<0, NM>([&](auto ic) { flush(ic); });
+    if (G == 32 && KT * BK != K) {  // half a K-tile: one group
+      const char* sa = smem + (KT - 1) % C::kA * C::OA::BYTES;
+      const char* sb = smem + C::B0 + ((KT - 1) & 1) * (C::BN * 128);
+      zero_acc<Tl>(grp);
+      static_for<0, NM>([&](auto ic) { Mma<T>::run(grp[ic / 2][ic % 2], fa[0][ic / 2], fb[0][ic % 2]); });
+#pragma unroll
+      for (int m = 0; m < Tl::FM; ++m) fa[1][m] = oa.frag(sa, m, 1);
+#pragma unroll
+      for (int f = 0; f < 2; ++f) fb[1][f] = *reinterpret_cast<const uint4*>(sb + foff[f][1]);
+      static_for<0, NM>([&](auto ic) { Mma<T>::run(grp[ic / 2][ic % 2], fa[1][ic / 2], fb[1][ic % 2]); });
+      scale(KT - 1, 0);
+      static_for<0, NM>([&](auto ic) { flush(ic); });
+    }
   }
   wait_vmcnt<0>();
   __syncthreads();

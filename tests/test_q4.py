@@ -125,6 +125,14 @@ def test_few_rows_of_many_groups(counts, N, K, G):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("K", [32, 64, 96, 160, 224, 320])
+def test_tiles_of_groups_of_32_that_end_in_half_a_k_tile(K):
+    for counts in ([20001], [9000, 0, 11001]):
+        print("case q4 half K-tile", K, len(counts), flush=True)
+        Case(counts, 264, K, 32, "bf16", "none", zeros=True).check()
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("G", [32, 64, 128])
 def test_tiles_of_ragged_groups(G):
     for epi in ("none", "swiglu"):
