@@ -249,8 +249,11 @@ __global__ __launch_bounds__(64 * kWaves) void q4_few_kernel(Q4Args qa) {
               }
             }
           }
+          // Past the end of K x is the last piece's again: 0 times an infinity there would be NaN. (bf16: it is NaN in
+          // its own place already.)
+          const bool on = BF || (round + n) * WS + ks < pieces;
 #pragma unroll
-          for (int c = 0; c < 4; ++c) acc[c] = __builtin_fmaf(s, BF ? dd[c] + oo[c] : dd[c], acc[c]);
+          for (int c = 0; c < 4; ++c) acc[c] = __builtin_fmaf(s, BF ? dd[c] + oo[c] : (on ? dd[c] : 0.0f), acc[c]);
         }
       });
       round += kBatch;

@@ -158,6 +158,34 @@ def test_infinite_weights_and_rows():
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("rows,N,K,group", [
+    (5, 72, 256, 64), (5, 24, 128, 128), (3, 40, 96, 32), (16, 136, 1088, 64), (3, 72, 1152, 128), (2, 24, 32, 32),  # few rows
+    ([4] * 40, 520, 288, 32), ([3, 0, 16] * 12, 520, 320, 64),                  # one and two waves on a tile of w
+    ([16, 3], 264, 2112, 64), ([16] * 12, 776, 2080, 32), ([16, 3, 16, 16] * 10, 1032, 2176, 128),  # x in stages
+    (700, 2056, 96, 32), (700, 520, 2112, 64), ([700, 3, 900], 1032, 640, 128)])  # tiles, also in slices of K
+def test_infinities_in_fp32_rows_are_the_formulas(rows, N, K, group):
+    """An infinity in x gives sum_k x w as fp32 arithmetic has it: an infinity of w's sign there, NaN where w is 0, wherever
+    in K it lies, the last piece of 128 of it included. It stays in its row."""
+    c = Case(rows, N, K, group, "f32", "none", True)
+    print("case q4 infinities", c.d.M, N, K, group, flush=True)
+    clean, want = c.forward(bias=False, res=False).cpu(), {}
+    for e in range(c.d.E):
+        at = [0, K // 2, K - 1, max(K - 128, 0), (K - 1) // 128 * 128]
+        for i, (r, k) in enumerate(zip(range(c.off[e], c.off[e + 1]), at)):
+            inf = float("inf") if (i + e) % 2 else -float("inf")
+            c.x[r, k] = inf
+            w = c.s[e, :, k // group] * (c.code[e, :, k].float() - c.z[e, :, k // group].float())
+            want[r] = w * inf
+    got = c.forward(bias=False, res=False).cpu()
+    keep = torch.ones(c.d.M, dtype=torch.bool)
+    for r, v in want.items():
+        keep[r] = False
+        assert torch.equal(torch.isnan(got[r]), torch.isnan(v)), r
+        assert torch.equal(torch.nan_to_num(got[r], nan=0.0), torch.nan_to_num(v, nan=0.0)), r
+    assert torch.equal(got[keep], clean[keep])
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("group", [32, 64, 128])
 def test_every_code_and_zero_point_alone(group):
     """x = one unit vector: y is s (code - z) exactly (bf16: |code - z| s has at most 12 bits, rounded once)."""
