@@ -655,10 +655,13 @@ mok_status mok_q4_quantize(const mok_q4_desc* d, const void* w, void* q, void* s
 
 /*
  * mok_q4_forward -- p = x_r w[e]^T + bias[e];  y_r = f(p) + res_r, in fp32, rounded once; w enters as the exact
- * values of its codes and scales.  off as of mok_grouped_desc; NULL (E = 1 only): one group of all M rows.
+ * values of its codes and scales (fp32, some shapes: as s (code - z) rounded to fp32).  off as of
+ * mok_grouped_desc; NULL (E = 1 only): one group of all M rows.
  * x [M][K], bias [E][P] fp32 or NULL, res [M][N] or NULL (may be the same array as y), y [M][N].
- * Up to some dozens of rows a group, bf16 x is multiplied by 16 + code and by 16 + z, whose difference is
- * exact but for fp32's sums: an infinity in x gives NaN there, and sums of 32 |x| have to stay below 3.4e38.
+ * A group's sum may be formed before it takes its scale: sums of 15 |x| over a group have to stay below 3.4e38.
+ * bf16: which of two kernels a call takes goes by its shape alone, and at any number of rows it can be the one that
+ * multiplies x by 16 + code and by 16 + z. Their difference is exact but for fp32's sums: an infinity in x then
+ * gives NaN in its row (else what the formula gives), and sums of 32 |x| have to stay below 3.4e38.
  */
 mok_status mok_q4_forward(const mok_q4_desc* d, const void* x, const void* q, const void* s, const uint8_t* z,
                           const float* bias, const int32_t* off, const void* res, void* y, void* ws, size_t ws_bytes,

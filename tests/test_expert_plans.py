@@ -215,6 +215,26 @@ def test_4bit_tiles_keep_to_their_rows_and_groups(act, epi, rows, N, K, G):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("M,N,K,G,few", [(5, 72, 256, 64, True), (600, 72, 256, 64, True), (2048, 264, 544, 32, True),
+                                         (4096, 136, 128, 128, True), (390, 2056, 128, 128, False), (700, 520, 2112, 64, False)])
+def test_4bit_infinity_in_a_bf16_row(M, N, K, G, few):
+    """The kernel for few rows, which small matrices take at any number of rows, gives NaN in that row, tiles an infinity of
+    w's sign and NaN where w is 0."""
+    assert (q4_split(BF16, "none", M, N, K) == 0) == few
+    c = Q4(M, N, K, G, BF16, "none", True)
+    clean = c.forward(bias=False, res=False).cpu()
+    c.x[3, K - 1] = float("inf")
+    got = c.forward(bias=False, res=False).cpu()
+    w = c.s[0, :, -1].float() * (c.code[0, :, -1].float() - c.z[0, :, -1].float())
+    want = torch.full((N,), float("nan")) if few else w * float("inf")
+    assert torch.equal(torch.isnan(got[3]), torch.isnan(want))
+    assert torch.equal(torch.nan_to_num(got[3].float(), nan=0.0, posinf=1.0, neginf=-1.0),
+                       torch.nan_to_num(want, nan=0.0, posinf=1.0, neginf=-1.0))
+    got[3] = clean[3]
+    assert torch.equal(got, clean)
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("act,epi,rows,N,K,G", [SLICED[2], SLICED[4], SLICED[12], SLICED[34], *TILED[1:3]])
 def test_4bit_tiles_in_place_captured_and_on_another_stream(act, epi, rows, N, K, G):
     """The residual's array as the output's, a stream of its own, and two graphs that share the slices' workspace."""
