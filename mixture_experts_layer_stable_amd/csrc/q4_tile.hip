@@ -23,7 +23,7 @@ __device__ __forceinline__ void dma4_any(const void* p, uint32_t lds) {
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, off" ::"s"(lds), "v"(p) : "memory", "m0");
 }
 
-template <typename T, class Tl, bool SW>
+template <typename T, class Tl>
 struct Q4Tile {
   using OA = DenseK<T, Tl::BM, Tl::FM, Tl::NW>;
   static constexpr int BN = 128;
@@ -37,7 +37,7 @@ struct Q4Tile {
 
 template <typename T, class Tl, bool SW, int G>
 __global__ __launch_bounds__(Tl::NT, sizeof(T) == 2 ? 2 : 1) void q4_tile_kernel(Q4Args qa) {
-  using C = Q4Tile<T, Tl, SW>;
+  using C = Q4Tile<T, Tl>;
   constexpr bool BF = std::is_same<T, bf16>::value;
   constexpr int ES = sizeof(T), BK = 128 / ES;      // values of a K-tile
   constexpr int GP = BK / G > 0 ? BK / G : 1;       // scales of a row in a K-tile
@@ -171,12 +171,13 @@ __global__ __launch_bounds__(Tl::NT, sizeof(T) == 2 ? 2 : 1) void q4_tile_kernel
       }
     }
   } else {
-    // One wave a SIMD: everything has its place between two matrix instructions, as in dense_tile. At a
+    // Two waves a SIMD, of two workgroups: everything has its place between two matrix instructions, as in dense_tile. At a
     // K-tile's last step the wave holds its fragments of it: it waits for its loads of the next and for
     // the workgroup, reads the next one's first fragments and loads x two, codes three K-tiles ahead. In
     // the other steps the next K-tile's codes become operands. A group's sums go to acc where the next
     // group's first products would overwrite them.
     constexpr int NM = Tl::FM * 2, NR = Tl::FM + 2;
+    static_assert(NM == 4, "slots 1 to 8 lie before the step that reads the operands");
     f32x16_t grp[Tl::FM][2];
     zero_acc<Tl>(grp);
     uint4 fa[2][Tl::FM], fb[2][2];
@@ -243,12 +244,12 @@ __global__ __launch_bounds__(Tl::NT, sizeof(T) == 2 ? 2 : 1) void q4_tile_kernel
             if constexpr (i < 2) fb[c ^ 1][i] = *reinterpret_cast<const uint4*>(sb + foff[i][(ks + 1) & 3]);
             else fa[c ^ 1][i - 2] = oa.frag(sa, i - 2, (ks + 1) & 3);
           }
-          // the next K-tile's operands: 32 codes, two at a time from slot 4 on
+          // the next K-tile's operands: 32 codes in slots 1 to 8, four in each
           if constexpr (slot == 0) {
             w = *reinterpret_cast<const uint4*>(raw + 16 * tid);
             zr = *reinterpret_cast<const uint32_t*>(raw + 4096 + 1024 + 4 * tid);
           }
-          constexpr int kFirst = NM == 8 ? 4 : 1, kPer = NM == 8 ? 1 : 2;  // first slot, pairs a slot
+          constexpr int kFirst = 1, kPer = 2;  // first slot, pairs a slot
           if constexpr (slot == kFirst) {
             const uint32_t ix = sg_lo + min(nk * BK / G + (GP > 1 ? part : 0), KG - 1);
             z = qa.zeros ? (float)(zr >> ((ix & 3) * 8) & 0xFFu) : 8.0f;
