@@ -7,8 +7,13 @@ namespace mok {
 
 namespace {
 
-// Rows of more than 16 MB an array are stored past the caches, which could not keep them for a reader.
-constexpr int64_t kNtBytes = 16 << 20;
+// Bytes of the rows that a call reads and writes, from which on it stores past the caches. The last one holds 256 MiB, and
+// what was written stays there for its reader where it fits beside what was read. Through the caches and past them, k = 8,
+// H = 7168, 16 experts: dispatch and the grouped product with 256 columns that reads xs, 22 MB of xs 66 and 92 us, 59 MB
+// 73 and 102, 117 MB 92 and 118, 176 MB (198 in all) 130 and 137, 235 MB (264 in all) 172 and 163, 1.9 GB 1189 and 1140;
+// combine's backward and its reader, 117 MB of d_o (250 in all) 123 and 135, 176 MB (375 in all) 173 and 169. The writer
+// alone takes up to 2 us less past the caches.
+constexpr int64_t kNtBytes = 256000000;
 
 template <bool NT>
 __device__ __forceinline__ void put_row(void* p, const uint4& v) {
@@ -118,7 +123,7 @@ unsigned blocks_of(int64_t n) { return (unsigned)std::min<int64_t>(n, 1 << 22); 
 template <typename T>
 hipError_t run_combine(const PermuteArgs& a, hipStream_t s) {
   const int64_t n = a.T * (a.H / Elem<T>::VE);
-  const bool nt = (int64_t)sizeof(T) * a.T * a.H > kNtBytes;
+  const bool nt = (int64_t)sizeof(T) * (a.R + a.T) * a.H > kNtBytes;
   const dim3 grid(blocks_of((n + 255) / 256)), block(256);
   if (nt) hipLaunchKernelGGL((combine_kernel<T, true>), grid, block, 0, s, a);
   else hipLaunchKernelGGL((combine_kernel<T, false>), grid, block, 0, s, a);
@@ -127,7 +132,7 @@ hipError_t run_combine(const PermuteArgs& a, hipStream_t s) {
 
 template <typename T>
 hipError_t run_combine_bwd(const PermuteArgs& a, hipStream_t s) {
-  const bool nt = (int64_t)sizeof(T) * a.R * a.H > kNtBytes;
+  const bool nt = (int64_t)sizeof(T) * (a.R * (a.dgate != nullptr ? 2 : 1) + a.T) * a.H > kNtBytes;
   const int lanes = row_lanes(a.H / Elem<T>::VE);
   const int64_t items = a.T * a.k + (a.perm != nullptr ? a.R : 0), per = 256 >> lanes;
   const dim3 grid(blocks_of((items + per - 1) / per)), block(256);
@@ -143,7 +148,7 @@ hipError_t launch_dispatch(const PermuteArgs& a, int act, hipStream_t s) {
   const int lanes = row_lanes(row_vecs);
   const int64_t per = 256 >> lanes;
   const dim3 grid(blocks_of((a.R + per - 1) / per)), block(256);
-  if (16 * a.R * row_vecs > kNtBytes) hipLaunchKernelGGL((dispatch_kernel<true>), grid, block, 0, s, a, row_vecs, lanes);
+  if (16 * (a.R + a.T) * row_vecs > kNtBytes) hipLaunchKernelGGL((dispatch_kernel<true>), grid, block, 0, s, a, row_vecs, lanes);
   else hipLaunchKernelGGL((dispatch_kernel<false>), grid, block, 0, s, a, row_vecs, lanes);
   return hipGetLastError();
 }

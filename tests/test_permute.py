@@ -96,6 +96,45 @@ def test_batch():
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("act,T", [("bf16", 1000), ("bf16", 2300), ("f32", 500), ("f32", 1150)])
+def test_rows_that_the_last_cache_holds_and_more(act, T):
+    """Less and more than 256 MB of rows in a call, which are stored in two ways. Small integers and gates that are powers of
+    two: every output is exact, in bf16 (8 bits) too."""
+    mok = _mok()
+    k, H, t = 8, 7168, mok.TORCH_DTYPE[mok.DTYPES[act]]
+    print("case permute caches", act, T, flush=True)
+    g = torch.Generator(device=DEV).manual_seed(T)
+    R = T * k + 5
+    rows = torch.randperm(R, generator=g, device=DEV)[:T * k]
+    live = torch.rand(T * k, generator=g, device=DEV) >= 0.1
+    perm = torch.full((R,), -1, dtype=torch.int32, device=DEV)
+    perm[rows[live]] = torch.arange(T * k, device=DEV)[live].int()
+    inv = torch.where(live, rows, torch.full_like(rows, -1)).int().view(T, k)
+    x = torch.randint(-4, 5, (T, H), generator=g, device=DEV).to(t)
+    o = torch.randint(-4, 5, (R, H), generator=g, device=DEV).to(t)
+    gate = torch.exp2(torch.randint(-1, 2, (T, k), generator=g, device=DEV).float())
+    new = lambda *s, dtype=t: torch.full(s, KEEP, dtype=dtype, device=DEV)
+    d = mok.PermuteDesc(T, H, k, R, act=mok.DTYPES[act])
+    xs, y, dx, do, dg = new(R, H), new(T, H), new(T, H), new(R, H), new(T, k, dtype=torch.float32)
+    mok.dispatch_forward(d, x, perm, xs)
+    slot = perm.clamp(min=0).long()
+    on = (perm >= 0)[:, None]
+    assert torch.equal(xs, torch.where(on, x[slot // k], torch.zeros((), dtype=t, device=DEV)))
+    mok.combine_forward(d, o, inv, y, gate=gate)
+    mok.dispatch_backward(d, o, inv, dx, add=x)
+    wy, wdx, wdg = torch.zeros(T, H, device=DEV), x.float().clone(), torch.zeros(T, k, device=DEV)
+    for j in range(k):
+        v = o[inv[:, j].clamp(min=0).long()].float() * (inv[:, j] >= 0)[:, None]
+        wy += gate[:, j:j + 1] * v
+        wdx += v
+        wdg[:, j] = (v * x.float()).sum(1)
+    assert torch.equal(y, wy.to(t)) and torch.equal(dx, wdx.to(t))
+    mok.combine_backward(d, x, o, inv, do, gate=gate, dgate=dg, perm=perm)
+    assert torch.equal(do, torch.where(on, (gate.view(-1)[slot][:, None] * x[slot // k].float()).to(t), torch.zeros((), dtype=t, device=DEV)))
+    assert torch.equal(dg, wdg)
+
+
+@pytest.mark.gpu
 def test_without_rows_or_tokens():
     mok = _mok()
     for T, R in ((0, 0), (0, 5), (5, 0)):
