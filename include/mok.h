@@ -611,11 +611,11 @@ mok_status mok_grouped_forward(const mok_grouped_desc* d, const void* x, const v
 
 /*
  * mok_grouped_backward -- gradients of L = <dy, y>.  dp = dy f'(pre), rounded to act as mok_linear_backward's:
- *   dx_r = dp_r w[e] + dx_add_r,  dw[e] = sum_{r in e} dp_r^T x_r + dw_add[e],  db[e] = sum_{r in e} dp_r.
- * dx [M][K], dw [E][P][K] (fp32 with MOK_FLAG_WGRAD_F32) and db [E][P] fp32 may be NULL: that gradient is
- * then not formed (w is read for dx only, x for dw only).  dx_add, dw_add may be NULL and may be the
- * same arrays as dx and dw; no other overlap is allowed.  dw and db are written for empty groups too
- * (dw_add or 0, and 0).
+ *   dx_r = dp_r w[e] + dx_add_r,  dw[e] = sum_{r in e} dp_r^T x_r + dw_add[e],  db[e] = sum_{r in e} dp_r
+ * (before that rounding).  dx [M][K], dw [E][P][K] (fp32 with MOK_FLAG_WGRAD_F32) and db [E][P] fp32 may be
+ * NULL: that gradient is then not formed (w is read for dx only, x for dw only).  dx_add, dw_add may be NULL
+ * and may be the same arrays as dx and dw; no other overlap is allowed.  dw and db are written for empty
+ * groups too (dw_add or 0, and 0).
  */
 mok_status mok_grouped_backward(const mok_grouped_desc* d, const void* dy, const void* pre, const void* x,
                                 const void* w, const int32_t* off, const void* dx_add, const void* dw_add, void* dx,

@@ -165,8 +165,9 @@ __global__ __launch_bounds__(Tl::NT) void grouped_dense_kernel(GroupedArgs ga) {
     a.b = (const T*)a.b + (int64_t)t.g * (KIND == LIN_FWD ? P * a.K : a.K * a.N);
     if (KIND == LIN_FWD && a.bias != nullptr) a.bias += t.g * P;
     // 256 x 256 tiles: a group's rows are shared out evenly, and its tiles are as high as that needs (64, 128, 192 or
-    // 256): they run side by side at one pace and take w from L2. Where a group's last tile alone was lower it ran
-    // ahead, and w came from HBM once for each (320 rows a group, 48 of 4096 x 7168: 1063 us).
+    // 256): they run side by side at one pace and share w (16384 rows of 42 groups, 4096 x 7168: 2.86 GB are read from
+    // memory, where w and x are 2.70). Where a group's last tile alone was lower: 1133 us for 1045 there, 1063 for 1008
+    // with 320 rows in each of 48 groups.
     constexpr bool CUT = Tl::BM == 256;
     const int64_t KT = (a.K + Cfg::BKE - 1) / Cfg::BKE;
     const int high = CUT ? (t.hi - t.lo + t.tiles - 1) / t.tiles : Tl::BM;

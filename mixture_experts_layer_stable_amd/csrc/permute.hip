@@ -23,8 +23,9 @@ __device__ __forceinline__ void put_row(void* p, const uint4& v) {
 }
 
 // out[r] = in[perm[r] / k], zeros for no slot. 2^lanes lanes copy a row, four vectors of it in flight. 16384 x 8
-// x 7168: 489 us (529 on another card, where stores through the caches took 564), 4.0 TB/s of each x read once: the experts' order reads every
-// row of x eight times, far apart, and x (235 MB) does not stay in the last cache beside what is written.
+// x 7168: 488 to 512 us over several cards (through the caches 557). The experts' order reads every row of x eight times,
+// far apart, and x (235 MB) stays in the last cache for some of them only: 1.38 GB come from memory and 1.88 GB go
+// there (traffic counters), 6.6 TB/s.
 template <bool NT>
 __global__ __launch_bounds__(256) void dispatch_kernel(PermuteArgs a, int row_vecs, int lanes) {
   const int step = 1 << lanes, v0 = threadIdx.x & (step - 1);

@@ -77,8 +77,9 @@ hipError_t launch_q4_quantize(const void* w, int64_t rows, int K, int group, int
 // of a group take for a million codes (up to 2^27 rows, whose tiles GroupScan counts). Tiles: K-tiles (of 64,
 // fp32 32) one after the other, half as long on an empty chip as on a full one, in rounds of 512 (fp32 256);
 // slices of K, of a dense product only (a second launch that adds them would have to know the rows' groups),
-// cost their partial products' way to memory and back. 2 x 2048 x 7168, measured: 64 rows 35 us, 128 36, 256 39,
-// 512 64, 1024 98; the few-row kernel takes 31 for 32 rows and as long again for each 32 more.
+// cost their partial products' way to memory and back. 2 x 2048 x 7168, measured on two cards: 64 rows 28 to 35 us,
+// 128 31 to 36, 256 39 to 41, 512 62, 1024 98 to 103; the few-row kernel takes 19 for 16 rows, and 31 for 32 where tiles in
+// slices, which those take now, need 25. The quantiser: 8 x 4096 x 7168 in 160 to 165 us bf16 (3.6 to 3.7 TB/s), 183 to 193 fp32 (5.6 to 5.8).
 int q4_split(int act, int epi, int64_t M, int N, int K, int E) {
   if (M == 0) return 0;
   const bool f32 = act == MOK_F32;

@@ -3,8 +3,10 @@
 //   p[m][n] = sum over groups j of K of s[n][j] (sum_k x[m][k] (16 + q[n][k]) - (16 + z[n][j]) sum_k x[m][k])
 //
 // What bounds them is, from some hundred MB of codes on, the instructions that a code takes (128 rows of 48
-// groups, 7168 x 2048: 85 us, 3.6 TB/s; 2 x 2048 x 7168 each: 143 us, 4.1 TB/s), and in small calls the
-// latency of each step, of which the loop is less than half (one row, 2 x 2048 x 7168: 9.6 us). A
+// groups, 7168 x 2048: 84 to 91 us, 3.5 TB/s; 2 x 2048 x 7168 each: 143 to 168 us, 3.6 to 4.1 TB/s), and in small calls the
+// latency of each step, of which the loop is less than half (one row, 2 x 2048 x 7168: 8.8 to 10.0 us; fp32 19.5). Dense
+// products of more rows load and convert each code again for every 16 of them: from 8 rows of 2 x 2048 x 7168, and from the
+// first of 7168 x 2048, the bf16 product of linear.hip is the faster one (16 rows: 19 and 15 us, 12 and 9). A
 // wave takes 16 rows of w (8 gate and 8 up rows for SWIGLU) and 128 codes of each at a time; four such
 // pieces are on their way while the four before them are worked on. Of a workgroup's eight waves WS share
 // a row tile, each a part of K, and 8 / WS tiles lie side by side. The workgroups, one a CU, share the tiles

@@ -6,10 +6,11 @@
 // exact in bf16, and the sums of each K-tile (of each group of 32, where a scale ends inside it) take their
 // scale in fp32, so w is never rounded. fp32: the operand is s (q - z), rounded once.
 // What bounds it is vector instructions beside the MFMAs: the codes' conversion, which every row tile
-// does again, and the sums' scaling. 4096 rows, 2 x 2048 x 7168: 322 us (747 TFLOP/s); 7168 x 2048: 169, in groups of 32
-// 189 (twice the scalings; with last K-tiles that branched around their loads, and spilled, 192 and 307). The sums are as many registers again as the
-// accumulators: 256 x 128 tiles spill (387 for the 333), 128 x 128 with one workgroup a CU take 0.79 us
-// a K-tile where two take 1.45 for both. fp32, 4096 rows, 2048 x 2048: 311 us (110 TFLOP/s).
+// does again, and the sums' scaling: the MFMAs are busy a third of the time. 4096 rows, 2 x 2048 x 7168: 322 to 342 us
+// over several cards (703 to 747 TFLOP/s); 7168 x 2048: 169 to 178, in groups of 32 189 to 193 (twice the scalings; with last
+// K-tiles that branched around their loads, and spilled, 192 and 307 where these took 169 and 189). The sums are as many
+// registers again as the accumulators: 256 x 128 tiles spill (387 for 333 on that card), 128 x 128 with one workgroup a CU
+// take 0.79 us a K-tile where two take 1.45 for both. fp32, 4096 rows, 2048 x 2048: 311 to 313 us (110 TFLOP/s).
 // Few tiles of a dense product take slices of K, joined by linear_join (128 rows, 2 x 2048 x 7168: 101 -> 36 us).
 #include "linear_dense.h"
 #include "q4.h"
